@@ -39,6 +39,21 @@ __all__ = [
     "fc_kv_redundancy",
     "fc_kv_score_topb",
     "fc_kv_compact",
+    "FC_ROPE_HALF",
+    "FC_ROPE_INTERLEAVED",
+    "FC_ROPE_PLAIN",
+    "FC_ROPE_LINEAR",
+    "FC_ROPE_NTK",
+    "FC_ROPE_YARN",
+    "RopePlan",
+    "fc_rope_init",
+    "fc_rope",
+    "Kv4Cache",
+    "fc_kv4_cache",
+    "fc_kv4_store",
+    "fc_kv4_load",
+    "fc_kv4_attention",
+    "fc_kv4_attention_workspace_size",
     "fc_gate_workspace_size",
     "fc_importance_workspace_size",
     "fc_redundancy_workspace_size",
@@ -60,6 +75,21 @@ class FlowCacheError(RuntimeError):
     def __init__(self, msg, status=None):
         super().__init__(msg)
         self.status = status
+
+
+class RopePlan(ctypes.Structure):
+    """``fc_rope_plan``: what :func:`fc_rope_init` fills and the calls read."""
+
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("reserved", ctypes.c_int32), ("m", ctypes.c_double),
+                ("turns", ctypes.c_double * 128), ("axis", ctypes.c_uint8 * 128)]
+
+
+class _Kv4(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("N", ctypes.c_int32), ("H", ctypes.c_int32), ("cap", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("k_exp", ctypes.c_int32), ("v_exp", ctypes.c_int32)]
 
 
 def _declare(lib):
@@ -93,6 +123,16 @@ def _declare(lib):
         "fc_kv_cache_commit": (c_int, [c_p, c_p, c_p, c_p, c_p, c_int, c_int, c_int, c_int, c_int,
                                        c_int, c_int, c_f, c_int, c_f, c_p, c_p, c_sz,
                                        ctypes.POINTER(c_int), ctypes.POINTER(c_int), c_p]),
+        "fc_rope_init": (c_int, [c_p, c_int, c_int, ctypes.c_double, c_int, ctypes.c_double, c_i64,
+                                 ctypes.c_double, ctypes.c_double, c_int, c_p]),
+        "fc_rope": (c_int, [c_p, c_p, c_int, c_int, c_int, c_int, c_int, c_p, c_p, c_p, c_p, c_int,
+                            c_p]),
+        "fc_kv4_store": (c_int, [c_p, c_p, c_int, c_int, c_int, c_int, c_int, c_p, c_p, c_p, c_int,
+                                 c_int, c_p, c_p, c_p, c_p, c_p]),
+        "fc_kv4_load": (c_int, [c_p, c_p, c_p, c_int, c_int, c_p, c_p, c_int, c_p, c_p]),
+        "fc_kv4_attention_workspace_size": (c_sz, [c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
+        "fc_kv4_attention": (c_int, [c_p, c_p, c_p, c_int, c_int, c_int, c_int, c_int, c_int, c_p,
+                                     c_int, c_f, c_p, c_p, c_p, c_p, c_sz, c_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -298,3 +338,162 @@ def fc_kv_compact(k, v, idx, k_out, v_out, stream=None):
     st = library().fc_kv_compact(_p(k), _p(v), _dtype_code(k), H, Lk, d, _p(idx), B, _p(k_out),
                                   _p(v_out), _s(stream))
     _check("fc_kv_compact", st)
+
+
+# ---- rotary positions and the 4-bit cache ---------------------------------------
+FC_ROPE_HALF, FC_ROPE_INTERLEAVED = 0, 1
+FC_ROPE_PLAIN, FC_ROPE_LINEAR, FC_ROPE_NTK, FC_ROPE_YARN = 0, 1, 2, 3
+_I64x3 = ctypes.c_int64 * 3
+
+
+def _rows(t, name):
+    """(pointer, (N, H, L, d), strides) of a [N, H, L, d] or [H, L, d] tensor whose
+    rows are contiguous; the other strides are free."""
+    if not t.is_cuda:
+        raise FlowCacheError("tensor arguments must be CUDA tensors")
+    n = t.dim()
+    if n not in (3, 4):
+        raise FlowCacheError(f"{name} must be [N, H, L, d] or [H, L, d]")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise FlowCacheError(f"the rows of {name} must be contiguous")
+    shape = tuple(t.shape) if n == 4 else (1,) + tuple(t.shape)
+    return ctypes.c_void_p(t.data_ptr()), shape, _I64x3(st[0] if n == 4 else 0, st[-3], st[-2])
+
+
+def _ints(t, shape, name):
+    """Pointer of a contiguous int32 CUDA tensor of the given number of elements."""
+    if t.dtype != torch.int32:
+        raise FlowCacheError(f"{name} must be int32")
+    n = 1
+    for s in shape:
+        n *= s
+    if t.numel() != n:
+        raise FlowCacheError(f"{name} has {t.numel()} elements, not {n} ({list(shape)})")
+    return _p(t)
+
+
+def _first_row(row0, N):
+    """(host row, device rows) of a ``row0`` argument."""
+    if isinstance(row0, torch.Tensor):
+        return 0, _ints(row0, (N,), "row0")
+    return int(row0), None
+
+
+def _plan_args(rope, pos, N, L):
+    if rope is None:
+        return None, None
+    if pos is None:
+        raise FlowCacheError("a rotation needs pos")
+    return ctypes.byref(rope), _ints(pos, (rope.n_axes, N, L), "pos")
+
+
+def fc_rope_init(rot_dim, layout=FC_ROPE_HALF, base=10000.0, scaling=FC_ROPE_PLAIN, factor=1.0,
+                 orig_len=0, beta_fast=32.0, beta_slow=1.0, sections=None):
+    """A :class:`RopePlan` for rows whose first ``rot_dim`` elements are rotated.
+    ``sections``: the number of frequencies that follow each position axis (up to
+    three, summing to rot_dim / 2); None for one axis."""
+    plan = RopePlan()
+    axes = 1 if sections is None else len(sections)
+    sec = None if sections is None else (ctypes.c_int * axes)(*[int(s) for s in sections])
+    st = library().fc_rope_init(ctypes.byref(plan), int(rot_dim), int(layout), float(base),
+                                int(scaling), float(factor), int(orig_len), float(beta_fast),
+                                float(beta_slow), axes, sec)
+    _check("fc_rope_init", st)
+    return plan
+
+
+def fc_rope(x, y, pos, plan, inverse=False, stream=None):
+    """Rotary positions.  x, y [N, H, L, d] (or [H, L, d]), strided, y may be x;
+    pos [axes, N, L] int32.  ``inverse`` applies the transpose, which maps the
+    gradient of y to the gradient of x."""
+    xp, (N, H, L, d), xs = _rows(x, "x")
+    yp, yshape, ys = _rows(y, "y")
+    if yshape != (N, H, L, d) or y.dtype != x.dtype:
+        raise FlowCacheError("x and y must have the same shape and type")
+    rope, p = _plan_args(plan, pos, N, L)
+    st = library().fc_rope(xp, yp, _dtype_code(x), N, H, L, d, xs, ys, p, rope, 1 if inverse else 0,
+                            _s(stream))
+    _check("fc_rope", st)
+
+
+class Kv4Cache:
+    """A cache in 4 bits: codes [N, H, cap, d/2] and scales [N, H, cap, d/16], uint8,
+    for keys and for values.  Keeps the tensors alive; ``struct`` is the
+    ``fc_kv4_cache`` that the calls take."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, k_exp=0, v_exp=0):
+        N, H, cap, half = k_codes.shape
+        for t, last in ((k_codes, half), (v_codes, half), (k_scales, half // 8), (v_scales, half // 8)):
+            if t.dtype != torch.uint8 or tuple(t.shape) != (N, H, cap, last):
+                raise FlowCacheError("a cache has uint8 codes [N, H, cap, d/2] and scales [N, H, cap, d/16]")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.N, self.H, self.cap, self.d = N, H, cap, 2 * half
+        self.struct = _Kv4(_p(k_codes), _p(k_scales), _p(v_codes), _p(v_scales), N, H, cap, 2 * half,
+                           int(k_exp), int(v_exp))
+
+
+def fc_kv4_cache(N, H, cap, d, k_exp=0, v_exp=0, device=None):
+    """A zeroed :class:`Kv4Cache` of N sequences, H heads and cap rows (a multiple
+    of 16) of d elements."""
+    z = lambda last: torch.zeros(N, H, cap, last, dtype=torch.uint8, device=device or "cuda")  # noqa: E731
+    return Kv4Cache(z(d // 2), z(d // 16), z(d // 2), z(d // 16), k_exp, v_exp)
+
+
+def fc_kv4_store(k, v, cache, row0=0, idx=None, rope=None, pos=None, stream=None):
+    """Write k, v [N, H, L, d] (or [H, L, d]) as 4-bit rows from ``row0`` on (an int,
+    or [N] int32 on the device).  ``idx`` [N, H, B] int32 selects the rows written;
+    ``rope`` and ``pos`` rotate the keys on the way."""
+    kp, (N, H, L, d), ks = _rows(k, "k")
+    vp, vshape, vs = _rows(v, "v")
+    if vshape != (N, H, L, d) or v.dtype != k.dtype:
+        raise FlowCacheError("k and v must have the same shape and type")
+    host, dev = _first_row(row0, N)
+    B = 0 if idx is None else idx.shape[-1]
+    plan, p = _plan_args(rope, pos, N, L)
+    st = library().fc_kv4_store(kp, vp, _dtype_code(k), N, H, L, d, ks, vs,
+                                 None if idx is None else _ints(idx, (N, H, B), "idx"), B, host, dev,
+                                 plan, p, ctypes.byref(cache.struct), _s(stream))
+    _check("fc_kv4_store", st)
+
+
+def fc_kv4_load(cache, k_out, v_out, row0=0, stream=None):
+    """The numbers of rows row0 .. row0 + L of the cache into k_out, v_out
+    [N, H, L, d] (or [H, L, d])."""
+    kp, (N, H, L, d), ks = _rows(k_out, "k_out")
+    vp, vshape, vs = _rows(v_out, "v_out")
+    if vshape != (N, H, L, d) or v_out.dtype != k_out.dtype or (N, H, d) != (cache.N, cache.H, cache.d):
+        raise FlowCacheError("k_out and v_out must be [N, H, L, d] of the cache, of one type")
+    host, dev = _first_row(row0, N)
+    st = library().fc_kv4_load(ctypes.byref(cache.struct), kp, vp, _dtype_code(k_out), L, ks, vs, host,
+                                dev, _s(stream))
+    _check("fc_kv4_load", st)
+
+
+def fc_kv4_attention_workspace_size(dtype, N, Hq, Hkv, Lq, max_len, d):
+    return library().fc_kv4_attention_workspace_size(dtype, N, Hq, Hkv, Lq, max_len, d)
+
+
+def fc_kv4_attention(q, cache, lens, out, ws, max_len=None, causal=False, scale=0.0, lse=None,
+                     stream=None):
+    """Attention of q [N, Hq, Lq, d] (or [Hq, Lq, d]) over the cache.  lens: [N] int32
+    on the device, an int for all sequences, or None (max_len of each); max_len
+    bounds the lengths (cap if None).  out like q; lse [N, Hq, Lq] float32 or None;
+    ws from :func:`fc_kv4_attention_workspace_size`."""
+    qp, (N, Hq, Lq, d), qs = _rows(q, "q")
+    op, oshape, os_ = _rows(out, "out")
+    if oshape != (N, Hq, Lq, d) or out.dtype != q.dtype:
+        raise FlowCacheError("q and out must have the same shape and type")
+    if max_len is None:
+        max_len = cache.cap
+    lp = None
+    if isinstance(lens, torch.Tensor):
+        lp = _ints(lens, (N,), "lens")
+    elif lens is not None:
+        max_len = min(int(lens), int(max_len))
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != N * Hq * Lq):
+        raise FlowCacheError("lse must be [N, Hq, Lq] float32")
+    st = library().fc_kv4_attention(qp, ctypes.byref(cache.struct), lp, int(max_len), _dtype_code(q),
+                                     N, Hq, Lq, d, qs, 1 if causal else 0, float(scale), op, os_,
+                                     _p(lse), _p(ws), ws.numel() * ws.element_size(), _s(stream))
+    _check("fc_kv4_attention", st)

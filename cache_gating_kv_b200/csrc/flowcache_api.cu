@@ -1,5 +1,6 @@
 // C-ABI of libflowcache: argument validation on the host, then launches.
 // The declarations and their contracts are in include/flowcache.h.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -10,6 +11,7 @@
 #include "../../include/flowcache_selftest.h"
 #include "fc_common.cuh"
 #include "fc_kernels.h"
+#include "kv4.cuh"
 
 namespace fc {
 
@@ -130,6 +132,121 @@ CacheWs cache_ws(int H, int Lq, int B_budget, int C, int d) {
   w.score_ws = o;
   w.total = fc::align_up(o + fc::score_topb_ws_bytes(H, (int)cap), 256);
   return w;
+}
+
+// ---- rotary positions and the 4-bit cache ------------------------------------
+// Device memory of the current device, aligned.
+fc_status check_ptr_here(const void* p, const char* name) {
+  fc_status st = check_ptr(p, name);
+  if (st != FC_OK) return st;
+  cudaPointerAttributes a;
+  int dev = 0;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(FC_ERR_CUDA, "cannot tell the device of %s", name);
+  }
+  if (a.type == cudaMemoryTypeDevice && a.device != dev)
+    return fail(FC_ERR_INVALID_ARG, "%s is on device %d, the current one is %d", name, a.device, dev);
+  return FC_OK;
+}
+
+#define FC_TRY(x)                 \
+  do {                            \
+    fc_status _st = (x);          \
+    if (_st != FC_OK) return _st; \
+  } while (0)
+
+struct View {
+  fc::Strides st;
+  size_t span;  // bytes from the first element to behind the last
+};
+
+// Strides of a [N][H][L][d] tensor; an output's rows must be disjoint.
+fc_status check_view(const int64_t* strides, fc_dtype dtype, int N, int H, int L, int d,
+                     bool output, const char* name, View* out) {
+  const int64_t el = (int64_t)elem_bytes(dtype);
+  fc::Strides s = {(int64_t)H * L * d, (int64_t)L * d, d};
+  if (strides != nullptr) s = {strides[0], strides[1], strides[2]};
+  const int64_t dims[3] = {N, H, L};
+  int64_t st[3] = {s.n, s.h, s.l};
+  int64_t last = d;
+  for (int i = 0; i < 3; ++i) {
+    if (st[i] < 0 || st[i] > (INT64_MAX / 64) / (dims[i] > 0 ? dims[i] : 1))
+      return fail(FC_ERR_INVALID_ARG, "%s: stride %lld out of range", name, (long long)st[i]);
+    if (dims[i] > 1 && st[i] * el % 16 != 0)
+      return fail(FC_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes", name);
+    last += (dims[i] - 1) * st[i];
+  }
+  if (output) {  // each dimension steps over what the smaller ones span
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+      for (int j = i + 1; j < 3; ++j)
+        if (st[order[j]] < st[order[i]]) {
+          const int x = order[i];
+          order[i] = order[j];
+          order[j] = x;
+        }
+    int64_t reach = d;
+    for (int i = 0; i < 3; ++i) {
+      const int k = order[i];
+      if (dims[k] <= 1) continue;
+      if (st[k] < reach) return fail(FC_ERR_INVALID_ARG, "%s: rows overlap", name);
+      reach += (dims[k] - 1) * st[k];
+    }
+  }
+  out->st = s;
+  out->span = (size_t)(last * el);
+  return FC_OK;
+}
+
+fc_status check_sizes4(fc_dtype dtype, int N, int H, int L) {
+  if (dtype != FC_F32 && dtype != FC_BF16)
+    return fail(FC_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  if (N < 1 || H < 1 || L < 1) return fail(FC_ERR_INVALID_ARG, "sizes must be >= 1");
+  if ((int64_t)N * H > (1 << 20))
+    return fail(FC_ERR_INVALID_ARG, "N * H must be <= 2^20 (got %lld)", (long long)N * H);
+  return FC_OK;
+}
+
+fc_status check_plan(const fc_rope_plan* p) {
+  if (p == nullptr) return fail(FC_ERR_INVALID_ARG, "plan is NULL");
+  if (p->rot_dim < 2 || p->rot_dim % 2 != 0 || p->rot_dim > 2 * FC_ROPE_MAX_FREQ ||
+      (p->layout != FC_ROPE_HALF && p->layout != FC_ROPE_INTERLEAVED) || p->n_axes < 1 ||
+      p->n_axes > FC_ROPE_MAX_AXES)
+    return fail(FC_ERR_INVALID_ARG, "plan was not filled by fc_rope_init");
+  for (int i = 0; i < p->rot_dim / 2; ++i)
+    if (p->axis[i] >= p->n_axes)
+      return fail(FC_ERR_INVALID_ARG, "plan was not filled by fc_rope_init");
+  return FC_OK;
+}
+
+struct CacheSpans {
+  size_t codes, scales;
+};
+
+fc_status check_cache(const fc_kv4_cache* c, CacheSpans* out) {
+  if (c == nullptr) return fail(FC_ERR_INVALID_ARG, "cache is NULL");
+  if (c->N < 1 || c->H < 1 || (int64_t)c->N * c->H > (1 << 20))
+    return fail(FC_ERR_INVALID_ARG, "cache: N, H must be >= 1 and N * H <= 2^20");
+  if (c->d != 64 && c->d != 128)
+    return fail(FC_ERR_UNSUPPORTED, "cache: d must be 64 or 128 (got %d)", c->d);
+  if (c->cap < 16 || c->cap % 16 != 0)
+    return fail(FC_ERR_INVALID_ARG, "cache: cap must be a multiple of 16 (got %d)", c->cap);
+  if (c->k_exp < -64 || c->k_exp > 64 || c->v_exp < -64 || c->v_exp > 64)
+    return fail(FC_ERR_INVALID_ARG, "cache: k_exp and v_exp must be in [-64, 64]");
+  FC_TRY(check_ptr_here(c->k_codes, "cache k_codes"));
+  FC_TRY(check_ptr_here(c->k_scales, "cache k_scales"));
+  FC_TRY(check_ptr_here(c->v_codes, "cache v_codes"));
+  FC_TRY(check_ptr_here(c->v_scales, "cache v_scales"));
+  const size_t rows = (size_t)c->N * c->H * c->cap;
+  out->codes = rows * (c->d / 2);
+  out->scales = rows * (c->d / 16);
+  return FC_OK;
+}
+
+bool overlaps_cache(const fc_kv4_cache* c, const CacheSpans& s, const void* p, size_t n) {
+  return ranges_overlap(c->k_codes, s.codes, p, n) || ranges_overlap(c->v_codes, s.codes, p, n) ||
+         ranges_overlap(c->k_scales, s.scales, p, n) || ranges_overlap(c->v_scales, s.scales, p, n);
 }
 
 }  // namespace
@@ -503,6 +620,224 @@ fc_status fc_kv_cache_commit(const void* q, const void* k_buf, const void* v_buf
     *compressed = 1;
   }
   return st;
+}
+
+fc_status fc_rope_init(fc_rope_plan* plan, int rot_dim, fc_rope_layout layout, double base,
+                       fc_rope_scaling scaling, double factor, int64_t orig_len, double beta_fast,
+                       double beta_slow, int n_axes, const int* sections) {
+  fc::g_launches = 0;
+  if (plan == nullptr) return fail(FC_ERR_INVALID_ARG, "plan is NULL");
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > 2 * FC_ROPE_MAX_FREQ)
+    return fail(FC_ERR_INVALID_ARG, "rot_dim must be even and in [2, %d] (got %d)",
+                2 * FC_ROPE_MAX_FREQ, rot_dim);
+  if (layout != FC_ROPE_HALF && layout != FC_ROPE_INTERLEAVED)
+    return fail(FC_ERR_INVALID_ARG, "unknown layout %d", (int)layout);
+  if (!(base > 1.0) || !std::isfinite(base))
+    return fail(FC_ERR_INVALID_ARG, "base must be finite and > 1");
+  if ((int)scaling < FC_ROPE_PLAIN || (int)scaling > FC_ROPE_YARN)
+    return fail(FC_ERR_INVALID_ARG, "unknown scaling %d", (int)scaling);
+  if (scaling != FC_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(FC_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  if (scaling == FC_ROPE_YARN &&
+      (orig_len < 1 || !(beta_slow >= 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
+    return fail(FC_ERR_INVALID_ARG, "need orig_len >= 1 and beta_fast > beta_slow >= 0");
+  if (n_axes < 1 || n_axes > FC_ROPE_MAX_AXES || (sections == nullptr && n_axes != 1))
+    return fail(FC_ERR_INVALID_ARG, "n_axes must be in [1, %d], with sections when over 1",
+                FC_ROPE_MAX_AXES);
+  const int half = rot_dim / 2;
+  if (sections != nullptr) {
+    int64_t sum = 0;
+    for (int i = 0; i < n_axes; ++i) {
+      if (sections[i] < 0) return fail(FC_ERR_INVALID_ARG, "sections must be >= 0");
+      sum += sections[i];
+    }
+    if (sum != half)
+      return fail(FC_ERR_INVALID_ARG, "sections sum to %lld, not to rot_dim / 2 = %d",
+                  (long long)sum, half);
+  }
+  fc_rope_plan p = {};
+  p.rot_dim = rot_dim;
+  p.layout = layout;
+  p.n_axes = n_axes;
+  p.m = scaling == FC_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  if (scaling == FC_ROPE_NTK && rot_dim > 2)
+    base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+  const double two_pi = 6.283185307179586476925286766559;
+  int ax = 0, left = sections != nullptr ? sections[0] : half;
+  for (int i = 0; i < half; ++i) {
+    double w = std::pow(base, -2.0 * i / rot_dim) / two_pi;
+    if (scaling == FC_ROPE_LINEAR) w /= factor;
+    if (scaling == FC_ROPE_YARN) {
+      double k = ((double)orig_len * w - beta_slow) / (beta_fast - beta_slow);
+      k = k < 0.0 ? 0.0 : k > 1.0 ? 1.0 : k;
+      w = (1.0 - k) * (w / factor) + k * w;
+    }
+    while (left == 0) left = sections[++ax];
+    --left;
+    p.turns[i] = w;
+    p.axis[i] = (uint8_t)ax;
+  }
+  *plan = p;
+  return ok();
+}
+
+fc_status fc_rope(const void* x, void* y, fc_dtype dtype, int N, int H, int L, int d,
+                  const int64_t* x_strides, const int64_t* y_strides, const int32_t* pos,
+                  const fc_rope_plan* plan, int inverse, void* stream) {
+  NvtxRange _range("fc_rope");
+  fc::g_launches = 0;
+  FC_TRY(check_sizes4(dtype, N, H, L));
+  FC_TRY(check_plan(plan));
+  if (d < 8 || d > 256 || d % 8 != 0)
+    return fail(FC_ERR_INVALID_ARG, "d must be a multiple of 8 in [8, 256] (got %d)", d);
+  if (plan->rot_dim > d)
+    return fail(FC_ERR_INVALID_ARG, "rot_dim %d is over d %d", plan->rot_dim, d);
+  View vx, vy;
+  FC_TRY(check_view(x_strides, dtype, N, H, L, d, false, "x", &vx));
+  FC_TRY(check_view(y_strides, dtype, N, H, L, d, true, "y", &vy));
+  FC_TRY(check_ptr_here(x, "x"));
+  if (y != x) FC_TRY(check_ptr_here(y, "y"));
+  FC_TRY(check_ptr_here(pos, "pos"));
+  const bool same = x == y && (N == 1 || vx.st.n == vy.st.n) && (H == 1 || vx.st.h == vy.st.h) &&
+                    (L == 1 || vx.st.l == vy.st.l);
+  if (!same && ranges_overlap(x, vx.span, y, vy.span))
+    return fail(FC_ERR_INVALID_ARG, "x and y overlap (in place needs the same strides)");
+  if (ranges_overlap(pos, (size_t)plan->n_axes * N * L * 4, y, vy.span))
+    return fail(FC_ERR_INVALID_ARG, "pos and y overlap");
+  return launched(fc::launch_rope(x, y, dtype == FC_BF16, N, H, L, d, vx.st, vy.st, pos, *plan,
+                                  inverse != 0, static_cast<cudaStream_t>(stream)),
+                  "fc_rope");
+}
+
+fc_status fc_kv4_store(const void* k, const void* v, fc_dtype dtype, int N, int H, int L, int d,
+                       const int64_t* k_strides, const int64_t* v_strides, const int32_t* idx,
+                       int B, int row0, const int32_t* row0_dev, const fc_rope_plan* rope,
+                       const int32_t* pos, const fc_kv4_cache* cache, void* stream) {
+  NvtxRange _range("fc_kv4_store");
+  fc::g_launches = 0;
+  FC_TRY(check_sizes4(dtype, N, H, L));
+  CacheSpans cs;
+  FC_TRY(check_cache(cache, &cs));
+  if (N != cache->N || H != cache->H || d != cache->d)
+    return fail(FC_ERR_INVALID_ARG, "N, H, d = %d, %d, %d are not the cache's %d, %d, %d", N, H, d,
+                cache->N, cache->H, cache->d);
+  if (idx != nullptr && B < 1) return fail(FC_ERR_INVALID_ARG, "B must be >= 1 (got %d)", B);
+  if (row0_dev == nullptr && row0 < 0)
+    return fail(FC_ERR_INVALID_ARG, "row0 must be >= 0 (got %d)", row0);
+  if (rope != nullptr) {
+    FC_TRY(check_plan(rope));
+    if (rope->rot_dim > d)
+      return fail(FC_ERR_INVALID_ARG, "rot_dim %d is over d %d", rope->rot_dim, d);
+    if (idx != nullptr)
+      return fail(FC_ERR_UNSUPPORTED, "rope with idx: a selection reads rows that are rotated already");
+    FC_TRY(check_ptr_here(pos, "pos"));
+  }
+  View vk, vv;
+  FC_TRY(check_view(k_strides, dtype, N, H, L, d, false, "k", &vk));
+  FC_TRY(check_view(v_strides, dtype, N, H, L, d, false, "v", &vv));
+  FC_TRY(check_ptr_here(k, "k"));
+  FC_TRY(check_ptr_here(v, "v"));
+  if (idx != nullptr) FC_TRY(check_ptr_here(idx, "idx"));
+  if (row0_dev != nullptr) FC_TRY(check_ptr_here(row0_dev, "row0_dev"));
+  if (overlaps_cache(cache, cs, k, vk.span) || overlaps_cache(cache, cs, v, vv.span))
+    return fail(FC_ERR_INVALID_ARG, "k or v overlaps the cache");
+  return launched(fc::launch_kv4_store(k, v, dtype == FC_BF16, L, vk.st, vv.st, idx,
+                                       idx != nullptr ? B : L, row0, row0_dev, rope, pos, *cache,
+                                       static_cast<cudaStream_t>(stream)),
+                  "fc_kv4_store");
+}
+
+fc_status fc_kv4_load(const fc_kv4_cache* cache, void* k_out, void* v_out, fc_dtype dtype, int L,
+                      const int64_t* k_strides, const int64_t* v_strides, int row0,
+                      const int32_t* row0_dev, void* stream) {
+  NvtxRange _range("fc_kv4_load");
+  fc::g_launches = 0;
+  CacheSpans cs;
+  FC_TRY(check_cache(cache, &cs));
+  FC_TRY(check_sizes4(dtype, cache->N, cache->H, L));
+  if (row0_dev == nullptr && row0 < 0)
+    return fail(FC_ERR_INVALID_ARG, "row0 must be >= 0 (got %d)", row0);
+  View vk, vv;
+  FC_TRY(check_view(k_strides, dtype, cache->N, cache->H, L, cache->d, true, "k_out", &vk));
+  FC_TRY(check_view(v_strides, dtype, cache->N, cache->H, L, cache->d, true, "v_out", &vv));
+  FC_TRY(check_ptr_here(k_out, "k_out"));
+  FC_TRY(check_ptr_here(v_out, "v_out"));
+  if (row0_dev != nullptr) FC_TRY(check_ptr_here(row0_dev, "row0_dev"));
+  if (overlaps_cache(cache, cs, k_out, vk.span) || overlaps_cache(cache, cs, v_out, vv.span) ||
+      ranges_overlap(k_out, vk.span, v_out, vv.span))
+    return fail(FC_ERR_INVALID_ARG, "k_out / v_out overlap the cache or each other");
+  return launched(fc::launch_kv4_load(*cache, k_out, v_out, dtype == FC_BF16, L, vk.st, vv.st, row0,
+                                      row0_dev, static_cast<cudaStream_t>(stream)),
+                  "fc_kv4_load");
+}
+
+size_t fc_kv4_attention_workspace_size(fc_dtype dtype, int N, int Hq, int Hkv, int Lq,
+                                       int max_len, int d) {
+  if ((dtype != FC_F32 && dtype != FC_BF16) || N < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 ||
+      (int64_t)N * Hq > (1 << 20) || Lq < 1 || (int64_t)(Hq / Hkv) * Lq > INT32_MAX / 2 ||
+      max_len < 0 || (d != 64 && d != 128))
+    return 0;
+  return fc::kv4_attention_ws_bytes(dtype == FC_BF16, N, Hq, Hkv, Lq, max_len, d);
+}
+
+fc_status fc_kv4_attention(const void* q, const fc_kv4_cache* cache, const int32_t* lens,
+                           int max_len, fc_dtype dtype, int N, int Hq, int Lq, int d,
+                           const int64_t* q_strides, int causal, float scale, void* out,
+                           const int64_t* out_strides, float* lse, void* ws, size_t ws_bytes,
+                           void* stream) {
+  NvtxRange _range("fc_kv4_attention");
+  fc::g_launches = 0;
+  FC_TRY(check_sizes4(dtype, N, Hq, Lq));
+  CacheSpans cs;
+  FC_TRY(check_cache(cache, &cs));
+  if (N != cache->N || d != cache->d)
+    return fail(FC_ERR_INVALID_ARG, "N, d = %d, %d are not the cache's %d, %d", N, d, cache->N,
+                cache->d);
+  if (Hq % cache->H != 0)
+    return fail(FC_ERR_INVALID_ARG, "Hq %d is not a multiple of the cache's %d heads", Hq, cache->H);
+  if ((int64_t)(Hq / cache->H) * Lq > INT32_MAX / 2)
+    return fail(FC_ERR_INVALID_ARG, "too many query rows to a key head");
+  if (max_len < 0 || max_len > cache->cap)
+    return fail(FC_ERR_INVALID_ARG, "max_len must be in [0, cap = %d] (got %d)", cache->cap, max_len);
+  const size_t need = fc::kv4_attention_ws_bytes(dtype == FC_BF16, N, Hq, cache->H, Lq, max_len, d);
+  if (ws == nullptr || ws_bytes < need)
+    return fail(FC_ERR_WORKSPACE, "attention workspace needs %zu bytes", need);
+  View vq, vo;
+  FC_TRY(check_view(q_strides, dtype, N, Hq, Lq, d, false, "q", &vq));
+  FC_TRY(check_view(out_strides, dtype, N, Hq, Lq, d, true, "out", &vo));
+  FC_TRY(check_ptr_here(q, "q"));
+  FC_TRY(check_ptr_here(out, "out"));
+  FC_TRY(check_ptr_here(ws, "ws"));
+  if (lens != nullptr) FC_TRY(check_ptr_here(lens, "lens"));
+  const size_t lse_bytes = (size_t)N * Hq * Lq * sizeof(float);
+  if (lse != nullptr) {
+    FC_TRY(check_ptr_here(lse, "lse"));
+    if (ranges_overlap(lse, lse_bytes, q, vq.span) || ranges_overlap(lse, lse_bytes, out, vo.span) ||
+        ranges_overlap(lse, lse_bytes, ws, need) || overlaps_cache(cache, cs, lse, lse_bytes))
+      return fail(FC_ERR_INVALID_ARG, "lse overlaps another argument");
+  }
+  if (ranges_overlap(out, vo.span, q, vq.span) || ranges_overlap(out, vo.span, ws, need) ||
+      overlaps_cache(cache, cs, out, vo.span) ||
+      (lens != nullptr && ranges_overlap(lens, (size_t)N * 4, out, vo.span)))
+    return fail(FC_ERR_INVALID_ARG, "out overlaps another argument");
+  if (ranges_overlap(ws, need, q, vq.span) || overlaps_cache(cache, cs, ws, need))
+    return fail(FC_ERR_INVALID_ARG, "ws overlaps another argument");
+  if (!(scale > 0.0f)) scale = 1.0f / sqrtf((float)d);
+  fc::Kv4Attn a = {};
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.lens = lens;
+  a.qs = vq.st;
+  a.os = vo.st;
+  a.Hq = Hq;
+  a.Lq = Lq;
+  a.max_len = max_len;
+  a.bf16 = dtype == FC_BF16;
+  a.causal = causal != 0;
+  a.scale = scale;
+  return launched(fc::launch_kv4_attention(a, *cache, ws, static_cast<cudaStream_t>(stream)),
+                  "fc_kv4_attention");
 }
 
 fc_status fc_selftest_exp2(const float* x, float* y_mufu, float* y_poly, int n, void* stream) {

@@ -391,6 +391,199 @@ fc_status fc_kv_cache_commit(const void* q, const void* k_buf, const void* v_buf
                              int32_t* idx, void* ws, size_t ws_bytes, int* n_next,
                              int* compressed, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Rotary positions, and a cache held in 4 bits with the attention over it. */
+/* The pages leave the attention that reads the compressed cache to the     */
+/* model; these calls are the library's own.                                */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Conventions of the calls below, beside those at the top of this file
+ *   - Tensors have four dimensions, [N][H][L][d]: N sequences, H heads, L rows
+ *     of d numbers.  The d numbers of a row are contiguous; the strides of the
+ *     other three, in elements, are given as {sequence, head, row}, or NULL for
+ *     a dense [N][H][L][d].  Strides are >= 0 and multiples of 16 bytes.  The
+ *     rows of an output must be disjoint.
+ *   - Every pointer must belong to the device that is current.
+ *   - N, H, L >= 1.  N*H <= 2^20.
+ */
+
+/* Which elements of a row form the pair that frequency i rotates. */
+typedef enum {
+  FC_ROPE_HALF = 0,       /* elements i and i + rot_dim/2 */
+  FC_ROPE_INTERLEAVED = 1 /* elements 2i and 2i + 1       */
+} fc_rope_layout;
+
+/* How the frequencies are scaled for contexts longer than the trained one. */
+typedef enum {
+  FC_ROPE_PLAIN = 0,  /* base^(-2i/rot_dim)                                       */
+  FC_ROPE_LINEAR = 1, /* the same divided by `factor` (position interpolation)    */
+  FC_ROPE_NTK = 2,    /* base * factor^(rot_dim/(rot_dim-2)) in place of base     */
+  FC_ROPE_YARN = 3    /* by parts: see fc_rope_init                               */
+} fc_rope_scaling;
+
+#define FC_ROPE_MAX_FREQ 128
+#define FC_ROPE_MAX_AXES 3
+
+/* A host-side plan, filled by fc_rope_init and passed by pointer; it is read
+ * during the call only. */
+typedef struct {
+  int32_t rot_dim;                  /* elements of a row that are rotated       */
+  int32_t layout;                   /* fc_rope_layout                           */
+  int32_t n_axes;                   /* position axes                            */
+  int32_t reserved;
+  double m;                         /* factor on the rotated elements           */
+  double turns[FC_ROPE_MAX_FREQ];   /* turns per position of each frequency     */
+  uint8_t axis[FC_ROPE_MAX_FREQ];   /* the axis whose position it follows       */
+} fc_rope_plan;
+
+/*
+ * Fill a plan.  With theta_i = base^(-2i/rot_dim), frequency i turns by
+ * w_i = theta_i / (2 pi) per position, changed by `scaling`:
+ *   FC_ROPE_LINEAR  w_i / factor
+ *   FC_ROPE_NTK     base replaced by base * factor^(rot_dim/(rot_dim-2))
+ *                   (unchanged for rot_dim = 2)
+ *   FC_ROPE_YARN    k_i w_i + (1 - k_i) w_i / factor, with
+ *                   k_i = clamp((orig_len w_i - beta_slow) /
+ *                               (beta_fast - beta_slow), 0, 1),
+ *                   and the factor m = 0.1 ln(factor) + 1 (m = 1 otherwise)
+ * everything in float64.
+ *   rot_dim   even, in [2, 256]
+ *   base      > 1, finite
+ *   factor    >= 1, finite (ignored by FC_ROPE_PLAIN)
+ *   orig_len, beta_fast, beta_slow   FC_ROPE_YARN only: orig_len >= 1,
+ *             beta_fast > beta_slow >= 0
+ *   n_axes    1 to 3 position axes (a video token has frame, row and column)
+ *   sections  [n_axes] frequencies of each axis, in order, summing to
+ *             rot_dim/2; NULL (n_axes must then be 1) for one axis
+ * Errors -> FC_ERR_INVALID_ARG, the plan untouched.  No device is used.
+ */
+fc_status fc_rope_init(fc_rope_plan* plan, int rot_dim, fc_rope_layout layout, double base,
+                       fc_rope_scaling scaling, double factor, int64_t orig_len, double beta_fast,
+                       double beta_slow, int n_axes, const int* sections);
+
+/*
+ * Rotary positions.  For row l of sequence n and frequency i, with
+ * p = pos[axis_i][n][l] and the turn u = p * w_i (float64), the pair (a, b)
+ * becomes
+ *   (a c - b s, b c + a s),   c = m cos(2 pi u), s = m sin(2 pi u),
+ * c and s evaluated in float64 and rounded once to float32, each product and
+ * each sum rounded once to float32, the result rounded once to dtype.  Elements
+ * from rot_dim on are copied.  With `inverse` s is negated: that is the
+ * transpose of the rotation, so it is also its gradient (x = the gradient of y
+ * gives the gradient of x).
+ *
+ *   x, y    [N][H][L][d] dtype with strides; y may be x itself with the same
+ *           strides (in place), otherwise the memory they span must not overlap
+ *   d       a multiple of 8 in [8, 256], >= rot_dim
+ *   pos     [n_axes][N][L] int32, any values (negative ones turn backwards)
+ * Errors: bad sizes, strides, plan or pointers -> FC_ERR_INVALID_ARG.
+ */
+fc_status fc_rope(const void* x, void* y, fc_dtype dtype, int N, int H, int L, int d,
+                  const int64_t* x_strides, const int64_t* y_strides, const int32_t* pos,
+                  const fc_rope_plan* plan, int inverse, void* stream);
+
+/*
+ * A cache of keys and values held as 4-bit floating point with a scale for
+ * every 16 numbers: a row of d numbers is d/2 bytes of codes and d/16 bytes of
+ * scales.  A code is e2m1 (sign, 2 exponent bits, 1 mantissa bit: 0, .5, 1,
+ * 1.5, 2, 3, 4, 6 and their negatives), element 2i in the low half of byte i
+ * and 2i + 1 in the high half; a scale is e4m3 (no infinities, 0x7F and 0xFF
+ * are NaN).  Element j of a row stands for
+ *   code_j * scale_{j/16} * 2^exp,
+ * which float32 and bf16 hold exactly.
+ */
+typedef struct {
+  void* k_codes;  /* [N][H][cap][d/2]  */
+  void* k_scales; /* [N][H][cap][d/16] */
+  void* v_codes;
+  void* v_scales;
+  int32_t N, H;         /* sequences, key heads */
+  int32_t cap;          /* rows of a sequence; a multiple of 16 */
+  int32_t d;            /* 64 or 128 */
+  int32_t k_exp, v_exp; /* in [-64, 64]: moves the scales' range, 2^-9 to 448 */
+} fc_kv4_cache;
+
+/*
+ * Write L rows of keys and values (or the B selected ones) into the cache.
+ * Per group of 16 consecutive elements, with y = x * 2^-exp in float32 and
+ * a = max |y|:
+ *   scale = e4m3(min(a / 6, 448)),  code = e2m1(y / scale),
+ * both divisions rounded to float32, both conversions to nearest with ties to
+ * even, the second one saturating at 6 (so an infinity is stored as the largest
+ * number, 6 * 448).  A scale of zero has zero codes.  A group with a NaN gets a
+ * NaN scale.  Storing what fc_kv4_load returned gives the same bits again while
+ * the scales are normal (>= 2^-6).
+ *
+ *   k, v     [N][H][L][d] dtype with strides, N, H and d those of the cache
+ *   idx      NULL, or [N][H][B] int32: row r of the result is row idx[n][h][r]
+ *            of k and v (an index outside [0, L) gives a row of zeros, as in
+ *            fc_kv_compact); B >= 1
+ *   row0     first row written, >= 0; with row0_dev ([N] int32, or NULL)
+ *            sequence n starts at row0_dev[n] instead
+ *   rope, pos  NULL, or a plan and positions as for fc_rope: the keys are
+ *            rotated first, in float32, without another rounding.  Not together
+ *            with idx (a selection reads rows that are rotated already).
+ * Rows of the cache outside [row0, row0 + rows) are left as they were; rows
+ * that would fall outside [0, cap) are not written.  k and v must not overlap the cache.
+ * Errors: bad sizes, strides or pointers -> FC_ERR_INVALID_ARG; d not 64 or
+ * 128, or rope with idx -> FC_ERR_UNSUPPORTED.
+ */
+fc_status fc_kv4_store(const void* k, const void* v, fc_dtype dtype, int N, int H, int L, int d,
+                       const int64_t* k_strides, const int64_t* v_strides, const int32_t* idx,
+                       int B, int row0, const int32_t* row0_dev, const fc_rope_plan* rope,
+                       const int32_t* pos, const fc_kv4_cache* cache, void* stream);
+
+/*
+ * The numbers of L rows of the cache, for the calls that read K and V
+ * (fc_kv_importance, fc_kv_redundancy, fc_kv_compact): exact in both dtypes.
+ *   k_out, v_out  [N][H][L][d] dtype with strides
+ *   row0, row0_dev  as for fc_kv4_store; rows outside [0, cap) give zeros
+ * Errors as for fc_kv4_store.
+ */
+fc_status fc_kv4_load(const fc_kv4_cache* cache, void* k_out, void* v_out, fc_dtype dtype, int L,
+                      const int64_t* k_strides, const int64_t* v_strides, int row0,
+                      const int32_t* row0_dev, void* stream);
+
+/* Workspace bytes for fc_kv4_attention (0 for invalid sizes). */
+size_t fc_kv4_attention_workspace_size(fc_dtype dtype, int N, int Hq, int Hkv, int Lq,
+                                       int max_len, int d);
+
+/*
+ * Attention over the cache.  Query head h reads key head h / (Hq/H).  With
+ * len_n the length of sequence n and x_ij = scale * 2^k_exp * q_i . k_j,
+ *   out_i = 2^v_exp sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(x_ij),
+ *   lse_i = ln sum_j p_ij,
+ * over the keys j < len_n, or with `causal` over j <= len_n - Lq + i (the
+ * queries are the last Lq positions of the sequence).  A query that sees no key
+ * has out = 0 and lse = -inf.
+ *
+ *   q, out   [N][Hq][Lq][d] dtype with strides; out must not overlap q
+ *   cache    N and d as q; Hq a multiple of its H
+ *   lens     [N] int32 (device), or NULL: every sequence has max_len keys.
+ *            Values outside [0, max_len] are clamped.
+ *   max_len  in [0, cap], the longest length; the work is split by it
+ *   scale    <= 0 selects 1/sqrt(d)
+ *   lse      [N][Hq][Lq] float32 out, or NULL
+ *   ws       fc_kv4_attention_workspace_size() bytes; nothing is carried
+ *            between calls but bytes 0..3, an error word with the meaning of
+ *            fc_kv_importance's (zero it once; read it with
+ *            fc_check_workspace, FC_WS_IMPORTANCE)
+ * The codes enter the tensor cores as float16, which holds code * scale
+ * exactly.  Queries enter as float16 after a power of two per row (FC_F32: as a
+ * sum of two), probabilities as float16 (FC_F32: a sum of two); sums are
+ * float32.  What rows at and behind len_n hold is not used, NaN scales
+ * included; a NaN that a query sees makes its whole row NaN, and one that it
+ * does not see leaves it alone.
+ * Errors: bad sizes, strides or pointers -> FC_ERR_INVALID_ARG; d not 64 or 128
+ * -> FC_ERR_UNSUPPORTED; small ws -> FC_ERR_WORKSPACE.
+ */
+fc_status fc_kv4_attention(const void* q, const fc_kv4_cache* cache, const int32_t* lens,
+                           int max_len, fc_dtype dtype, int N, int Hq, int Lq, int d,
+                           const int64_t* q_strides, int causal, float scale, void* out,
+                           const int64_t* out_strides, float* lse, void* ws, size_t ws_bytes,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,3 +6,4 @@ may use it.
 """
 
 from .flowcache_oracle import *  # noqa: F401,F403
+from .kv4_oracle import *  # noqa: F401,F403
