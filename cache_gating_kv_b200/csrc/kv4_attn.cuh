@@ -1,8 +1,11 @@
 // What the kernels of the attention over the 4-bit cache share.
 #pragma once
 
+#include <cuda.h>
+
 #include "fc_common.cuh"
 #include "kv4.cuh"
+#include "tc_ptx.cuh"
 
 namespace fc {
 
@@ -36,6 +39,24 @@ __device__ __forceinline__ int block_keys(const AttnArgs& a, int len, int r0, in
   return row_keys(a, len, (min(r0 + rows, a.R) - 1) / a.G);
 }
 
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(reinterpret_cast<const __half2&>(a), reinterpret_cast<const __half2&>(b));
+  return reinterpret_cast<const uint32_t&>(r);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return reinterpret_cast<const uint32_t&>(r);
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          tc::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
 // Four outputs of row r from their weighted sums o, the row's log2 reference
 // and its sum L of 2^(x - ref).
 template <typename T>
@@ -57,5 +78,10 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int n, int hk, int 
     a.lse[((int64_t)n * a.Hkv * a.G + h) * a.Lq + i] = v;
   }
 }
+
+// The tensor-core kernel for many query rows (bf16): rows of a block, keys of a
+// tile.
+constexpr int kTcRows = 256, kTcKeys = 128;
+cudaError_t launch_attn_tc(const AttnArgs& a, int N, int d, cudaStream_t s);
 
 }  // namespace fc

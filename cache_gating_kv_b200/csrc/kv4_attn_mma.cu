@@ -40,7 +40,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;  // keys of a warp's step
-constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D> constexpr int step_bytes() { return kStep * (D + D / 8); }
 template <int D> constexpr int stages() { return D == 128 ? 3 : 5; }
@@ -62,27 +61,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(reinterpret_cast<const __half2&>(a), reinterpret_cast<const __half2&>(b));
-  return reinterpret_cast<const uint32_t&>(r);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 r = __floats2half2_rn(lo, hi);
-  return reinterpret_cast<const uint32_t&>(r);
-}
 // What float16 rounding left of (lo, hi).
 __device__ __forceinline__ uint32_t rest_f16(uint32_t h, float lo, float hi) {
   const float2 f = __half22float2(reinterpret_cast<const __half2&>(h));
   return pack_f16(lo - f.x, hi - f.y);
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          tc::smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
-      : "memory");
 }
 
 // D/4 consecutive elements of a query row as float32; zeros for a missing row.
@@ -485,24 +467,27 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
   }
 }
 
-// Shares of the key axis: enough blocks to fill the SMs (three resident blocks
-// each), at least 256 keys to a share.  With as many units as slots, or one
-// short history, there is nothing to split and the join is not launched.
-// n_most bounds n_split and does not fall with max_len: the workspace goes by it,
-// so one made for a length serves every shorter one.
-void choose_split(int64_t units, int max_len, int& n_split, int& chunk, int64_t& n_most) {
-  const int64_t slots = 3ll * sm_count();
-  n_split = 1;
-  n_most = 1;
-  chunk = max_len > 0 ? (int)align_up((size_t)max_len, 128) : 128;
-  if (max_len <= 512 || units >= 4 * slots) return;
-  // few units: one wave; many: three, so that unlike lengths even out
-  const int64_t want = units * 4 <= slots ? slots / units : ceil_div(3 * slots, units);
+// Shares of the key axis: enough blocks to fill the SMs, at least `least` keys to
+// a share.  With as many units as slots, or one short history, there is nothing to
+// split and the join is not launched.  n_most bounds n_split and does not fall
+// with max_len: the workspace goes by it, so one made for a length serves every
+// shorter one.
+struct Shares {
+  int n_split, chunk;
+  int64_t n_most;
+};
+Shares choose_split(int64_t units, int max_len, int64_t slots, int least, int64_t waves) {
+  Shares s = {1, max_len > 0 ? (int)align_up((size_t)max_len, 128) : 128, 1};
+  if (max_len <= 2 * least || units >= (waves > 1 ? 4 * slots : slots)) return s;
+  // few units: one wave; many: several, so that unlike lengths even out
+  const int64_t want = waves == 1 || units * 4 <= slots ? slots / units : ceil_div(waves * slots, units);
+  if (want <= 1) return s;
   const int64_t c = ceil_div(max_len, want);
-  chunk = (int)align_up((size_t)(c < 256 ? 256 : c), 128);
-  n_split = (int)ceil_div(max_len, chunk);
-  n_most = ceil_div(max_len, 256);
-  if (n_most > want) n_most = want;
+  s.chunk = (int)align_up((size_t)(c < least ? least : c), 128);
+  s.n_split = (int)ceil_div(max_len, s.chunk);
+  s.n_most = ceil_div(max_len, least);
+  if (s.n_most > want) s.n_most = want;
+  return s;
 }
 
 template <typename T, int D, int MT>
@@ -512,8 +497,7 @@ cudaError_t run(AttnArgs a, int N, cudaStream_t s) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (int64_t)N * a.Hkv * a.n_rb * a.n_split;
-  const int64_t rows = (int64_t)N * a.Hkv * a.R;
-  if (blocks > 0x7fffffffll || rows > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -525,18 +509,28 @@ cudaError_t run(AttnArgs a, int N, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<T, D, MT>, a);
   if (e != cudaSuccess) return e;
   add_launches(1);
-  if (a.n_split > 1) {
-    cfg.gridDim = dim3((unsigned)rows);
-    cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, a);
-    if (e != cudaSuccess) return e;
-    add_launches(1);
-  }
   return cudaGetLastError();
 }
 
-// Query rows of a block.
-int rows_of_block(bool bf16, int R) { return bf16 && R > 16 ? 32 : 16; }
+template <typename T, int D>
+cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
+  const int64_t rows = (int64_t)N * a.Hkv * a.R;
+  if (rows > 0x7fffffffll) return cudaErrorInvalidValue;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, a);
+  if (e != cudaSuccess) return e;
+  add_launches(1);
+  return cudaGetLastError();
+}
+
+// The tensor-core kernel takes over where its 256-row blocks are worth filling.
+bool use_tc(bool bf16, int R) { return bf16 && R > 64; }
 
 struct Layout {
   int rows_blk, n_rb, n_split, chunk;
@@ -545,15 +539,34 @@ struct Layout {
 Layout layout(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d) {
   Layout l;
   const int R = Hq / Hkv * Lq;
-  l.rows_blk = rows_of_block(bf16, R);
+  const bool tc = use_tc(bf16, R);
+  l.rows_blk = tc ? kTcRows : bf16 && R > 16 ? 32 : 16;
   l.n_rb = (int)ceil_div(R, l.rows_blk);
-  int64_t n_most;
-  choose_split((int64_t)N * Hkv * l.n_rb, max_len, l.n_split, l.chunk, n_most);
-  const size_t parts = n_most > 1 ? (size_t)N * Hkv * R * n_most : 0;
+  const int64_t units = (int64_t)N * Hkv * l.n_rb;
+  const Shares sh = tc ? choose_split(units, max_len, sm_count(), 512, 1)
+                       : choose_split(units, max_len, 3ll * sm_count(), 256, 3);
+  l.n_split = sh.n_split;
+  l.chunk = sh.chunk;
+  const size_t parts = sh.n_most > 1 ? (size_t)N * Hkv * R * sh.n_most : 0;
   l.ml = 256;
   l.o = align_up(l.ml + parts * sizeof(float2), 256);
   l.total = align_up(l.o + parts * d * sizeof(float), 256);
   return l;
+}
+
+template <int D>
+cudaError_t run_all(const AttnArgs& a, bool bf16, int N, cudaStream_t s) {
+  cudaError_t e;
+  if (!bf16)
+    e = run<float, D, 1>(a, N, s);
+  else if (a.rows_blk == kTcRows)
+    e = launch_attn_tc(a, N, D, s);
+  else if (a.rows_blk == 16)
+    e = run<__nv_bfloat16, D, 1>(a, N, s);
+  else
+    e = run<__nv_bfloat16, D, 2>(a, N, s);
+  if (e != cudaSuccess || a.n_split == 1) return e;
+  return bf16 ? join<__nv_bfloat16, D>(a, N, s) : join<float, D>(a, N, s);
 }
 }  // namespace
 
@@ -581,7 +594,7 @@ cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* 
   a.max_len = p.max_len;
   a.cap = c.cap;
   a.causal = p.causal;
-  a.scale_log2 = ldexpf(p.scale * kLog2e, c.k_exp);
+  a.scale_log2 = ldexpf(p.scale * 1.4426950408889634f, c.k_exp);
   a.out_scale = ldexpf(1.0f, c.v_exp);
   const Layout l = layout(p.bf16, c.N, p.Hq, c.H, p.Lq, p.max_len, c.d);
   a.rows_blk = l.rows_blk;
@@ -592,11 +605,7 @@ cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* 
   a.err = reinterpret_cast<int*>(w);
   a.part_ml = reinterpret_cast<float2*>(w + l.ml);
   a.part_o = reinterpret_cast<float*>(w + l.o);
-  if (!p.bf16)
-    return c.d == 128 ? run<float, 128, 1>(a, c.N, s) : run<float, 64, 1>(a, c.N, s);
-  if (l.rows_blk == 16)
-    return c.d == 128 ? run<__nv_bfloat16, 128, 1>(a, c.N, s) : run<__nv_bfloat16, 64, 1>(a, c.N, s);
-  return c.d == 128 ? run<__nv_bfloat16, 128, 2>(a, c.N, s) : run<__nv_bfloat16, 64, 2>(a, c.N, s);
+  return c.d == 128 ? run_all<128>(a, p.bf16, c.N, s) : run_all<64>(a, p.bf16, c.N, s);
 }
 
 }  // namespace fc
