@@ -59,8 +59,9 @@ fc_status ok() {
   return FC_OK;
 }
 
-// Null, misalignment and host-memory checks for one tensor argument.
-fc_status check_ptr(const void* p, const char* name) {
+// Null, misalignment and host-memory checks for one tensor argument; with `dev`
+// >= 0 also that it belongs to that device.
+fc_status check_ptr(const void* p, const char* name, int dev = -1) {
   if (p == nullptr) return fail(FC_ERR_INVALID_ARG, "%s is NULL", name);
   if (reinterpret_cast<uintptr_t>(p) % 16 != 0)
     return fail(FC_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
@@ -72,6 +73,8 @@ fc_status check_ptr(const void* p, const char* name) {
   }
   if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
     return fail(FC_ERR_INVALID_ARG, "%s is not device memory", name);
+  if (dev >= 0 && a.type == cudaMemoryTypeDevice && a.device != dev)
+    return fail(FC_ERR_INVALID_ARG, "%s is on device %d, the current one is %d", name, a.device, dev);
   return FC_OK;
 }
 
@@ -135,19 +138,14 @@ CacheWs cache_ws(int H, int Lq, int B_budget, int C, int d) {
 }
 
 // ---- rotary positions and the 4-bit cache ------------------------------------
-// Device memory of the current device, aligned.
+// Aligned memory of the current device.
 fc_status check_ptr_here(const void* p, const char* name) {
-  fc_status st = check_ptr(p, name);
-  if (st != FC_OK) return st;
-  cudaPointerAttributes a;
   int dev = 0;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+  if (p != nullptr && cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
-    return fail(FC_ERR_CUDA, "cannot tell the device of %s", name);
+    dev = -1;  // no device: the pointer query reports it
   }
-  if (a.type == cudaMemoryTypeDevice && a.device != dev)
-    return fail(FC_ERR_INVALID_ARG, "%s is on device %d, the current one is %d", name, a.device, dev);
-  return FC_OK;
+  return check_ptr(p, name, dev);
 }
 
 #define FC_TRY(x)                 \
