@@ -37,28 +37,49 @@
 namespace fc {
 
 namespace {
-constexpr int kWarps = 4;
+constexpr int kStep = 32;      // keys of a warp's step
+constexpr int kGroup = 4;      // warps that work on one stage
+constexpr int kWarps = 8;      // two groups, taking stages in turn
+constexpr int kGroups = kWarps / kGroup;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 32;  // keys of a warp's step
+constexpr int kStage = kGroup * kStep;
+constexpr int kJoinWarps = 4;
 
-template <int D> constexpr int step_bytes() { return kStep * (D + D / 8); }
-template <int D> constexpr int stages() { return D == 128 ? 3 : 5; }
-template <int D> constexpr int ring_bytes() { return step_bytes<D>() * stages<D>(); }
-template <int D, int MT> constexpr int merge_bytes() { return MT * 16 * (D + 2) * 4; }
-template <int D, int MT> constexpr int warp_bytes() {
-  return ring_bytes<D>() > merge_bytes<D, MT>() ? ring_bytes<D>() : merge_bytes<D, MT>();
+template <int D> constexpr int stage_bytes() { return kStage * (D + D / 8); }
+template <int D> constexpr int stages() { return D == 128 ? 5 : 8; }
+// Outputs of a row at the end, with two numbers beside them and an odd stride.
+template <int D, int NR> constexpr int warp_result_bytes() { return NR * 8 * (D + 4) * 4; }
+template <int D, int NR> constexpr int ring_bytes() {
+  const int ring = stages<D>() * stage_bytes<D>(), join = kWarps * warp_result_bytes<D, NR>();
+  return ring > join ? ring : join;
 }
-template <int D, int MT> constexpr int smem_bytes() {
-  return kWarps * warp_bytes<D, MT>() + kWarps * stages<D>() * 8;
+template <int D, int NR> constexpr int smem_bytes() {
+  return ring_bytes<D, NR>() + 2 * stages<D>() * 8;
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+// c = a b (+ c): m16n8k16, float16 operands, float32 sums.
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_add(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit numbers (thread 4 r + c / 2 holds row r, columns c, c + 1)
+// transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // What float16 rounding left of (lo, hi).
@@ -79,19 +100,18 @@ __device__ __forceinline__ void load_q(const T* p, bool have, float (&f)[E]) {
   }
 }
 
-// Two scale bytes (keys a and b, one group) as a float16 pair, zero where a key
-// is not used or its scale is NaN (the keys carry the NaN instead).
-__device__ __forceinline__ uint32_t value_scales(uint32_t a, uint32_t b, bool use_a, bool use_b) {
-  a = use_a && !kv4::scale_is_nan(a) ? a : 0u;
-  b = use_b && !kv4::scale_is_nan(b) ? b : 0u;
-  return kv4::e4m3x2_to_f16x2(a | (b << 8));
+// Bit 7 of each byte of the result: that byte of e4m3 is NaN.
+__device__ __forceinline__ uint32_t nan_bits(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
+// NR: tiles of 8 query rows.
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
+    attn_mma_kernel(const AttnArgs a) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int KS = D / 16;        // k16 steps of a logit
-  constexpr int NT = D / 8;         // n8 tiles of the output
+  constexpr int MT = D / 16;        // m16 tiles of the output
   constexpr int E = D / 4;          // elements of d that a thread holds of a key
   constexpr int CB = D / 2, SB = D / 16;
   constexpr int S = stages<D>();
@@ -101,8 +121,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * warp_bytes<D, MT>();
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kWarps * warp_bytes<D, MT>()) + warp * S;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes<D, NR>());
+  uint64_t* empty = full + S;
 
   int b = blockIdx.x;
   const int split = b % a.n_split;
@@ -111,302 +131,353 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
   const int unit = b / a.n_rb;  // n * Hkv + key head
   const int n = unit / a.Hkv, hk = unit % a.Hkv;
 
-  if (lane == 0) {
-    for (int s = 0; s < S; ++s) tc::mbar_init(&full[s], 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], kGroup);
+    }
     tc::fence_barrier_init();
   }
-  __syncwarp();
   grid_dep_wait();
   grid_dep_launch();
 
   const int len = seq_len(a, n);
-  const int r_base = rb * 16 * MT;
-  const int k_top = block_keys(a, len, r_base, 16 * MT);
+  const int r_base = rb * 8 * NR;
+  const int k_top = block_keys(a, len, r_base, 8 * NR);
   const int k_begin = split * a.chunk;
   const int k_end = min(k_top, k_begin + a.chunk);
   if (a.n_split > 1 && k_begin >= k_end) return;  // the join does not look for it
-  const int n_steps = k_begin < k_end ? (k_end - k_begin + kStep - 1) / kStep : 0;
+  const int n_stages = k_begin < k_end ? (k_end - k_begin + kStage - 1) / kStage : 0;
   const int k_pad = (k_end + 15) & ~15;  // rows are copied in sixteens (cap is a multiple)
 
   const int64_t head = (int64_t)unit * a.cap;
-  auto fetch = [&](int step) {  // lane 0: the copies of one of the warp's steps
-    const int s = (step / kWarps) % S;
-    const int k0 = k_begin + step * kStep;
-    const int rows = min(kStep, k_pad - k0);
-    uint8_t* dst = ring + s * step_bytes<D>();
+  auto fetch = [&](int i) {  // one thread: the copies of stage i
+    const int s = i % S;
+    const int k0 = k_begin + i * kStage;
+    const int rows = min(kStage, k_pad - k0);
+    uint8_t* dst = smem + s * stage_bytes<D>();
     tc::mbar_expect_tx(&full[s], rows * 2 * (CB + SB));
     bulk_load(dst, a.k_codes + (head + k0) * CB, rows * CB, &full[s]);
-    bulk_load(dst + kStep * CB, a.v_codes + (head + k0) * CB, rows * CB, &full[s]);
-    bulk_load(dst + 2 * kStep * CB, a.k_scales + (head + k0) * SB, rows * SB, &full[s]);
-    bulk_load(dst + kStep * (2 * CB + SB), a.v_scales + (head + k0) * SB, rows * SB, &full[s]);
+    bulk_load(dst + kStage * CB, a.v_codes + (head + k0) * CB, rows * CB, &full[s]);
+    bulk_load(dst + 2 * kStage * CB, a.k_scales + (head + k0) * SB, rows * SB, &full[s]);
+    bulk_load(dst + kStage * (2 * CB + SB), a.v_scales + (head + k0) * SB, rows * SB, &full[s]);
   };
-  if (lane == 0)
-    for (int i = 0; i < S; ++i)
-      if (warp + i * kWarps < n_steps) fetch(warp + i * kWarps);
+  if (threadIdx.x == 0)
+    for (int i = 0; i < S && i < n_stages; ++i) fetch(i);
 
-  // Queries: the fragment of k16 step s holds elements t E + 4 s .. + 3 of rows
-  // g and g + 8, times a power of two that brings the row's largest to 2^13.
-  uint32_t qa[MT][P][KS][4];
-  float fac[MT][2];   // of a logit, to base 2
-  int lim[MT][2];     // keys that the row sees
+  // Queries are the B operand: in k16 step s thread (g, t) holds elements
+  // t E + 4 s .. + 3 of row g, times a power of two that brings the row's largest
+  // to 2^13.  Logits come out with the rows on the columns, 2 t and 2 t + 1.
+  uint32_t qb[NR][P][KS][2];
+  float fac[NR][2];   // of a logit, to base 2
+  int lim[NR][2];     // keys that the row sees
   int lim_min = k_end;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int m = 0; m < NR; ++m) {
+    const int r = r_base + m * 8 + g;
+    const bool have = r < a.R;
+    const int i = r / a.G, hq = hk * a.G + r % a.G;
+    const int row_lim = have ? min(k_end, row_keys(a, len, i)) : k_end;
+    float f[E];
+    load_q<T, E>(reinterpret_cast<const T*>(a.q) + n * a.qs.n + hq * a.qs.h + i * a.qs.l + t * E,
+                 have, f);
+    float top = 0.0f;
 #pragma unroll
-    for (int hrow = 0; hrow < 2; ++hrow) {
-      const int r = r_base + m * 16 + hrow * 8 + g;
-      const bool have = r < a.R;
-      const int i = r / a.G, hq = hk * a.G + r % a.G;
-      lim[m][hrow] = have ? min(k_end, row_keys(a, len, i)) : 0;
-      lim_min = min(lim_min, have ? lim[m][hrow] : k_end);
-      float f[E];
-      load_q<T, E>(reinterpret_cast<const T*>(a.q) + n * a.qs.n + hq * a.qs.h + i * a.qs.l + t * E,
-                   have, f);
-      float top = 0.0f;
+    for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(f[e]));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    int ex = (int)(__float_as_uint(top) >> 23) - 127;
+    ex = top == 0.0f ? 0 : max(-100, min(ex, 127));
+    const float down = __uint_as_float((uint32_t)(127 + 13 - ex) << 23);
+    const float row_fac = fmaxf(ldexpf(a.scale_log2, ex - 13), 1.2e-38f);  // never 0 * -inf
 #pragma unroll
-      for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(f[e]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      int ex = (int)(__float_as_uint(top) >> 23) - 127;
-      ex = top == 0.0f ? 0 : max(-100, min(ex, 127));
-      const float down = __uint_as_float((uint32_t)(127 + 13 - ex) << 23);
-      fac[m][hrow] = fmaxf(ldexpf(a.scale_log2, ex - 13), 1.2e-38f);  // never 0 * -inf
+    for (int s = 0; s < KS; ++s) {
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const float lo = f[4 * s + 2 * w] * down, hi = f[4 * s + 2 * w + 1] * down;
-          const uint32_t h = pack_f16(lo, hi);
-          qa[m][0][s][2 * w + hrow] = h;
-          if constexpr (kF32) qa[m][P - 1][s][2 * w + hrow] = rest_f16(h, lo, hi);
-        }
+      for (int w = 0; w < 2; ++w) {
+        const float lo = f[4 * s + 2 * w] * down, hi = f[4 * s + 2 * w + 1] * down;
+        const uint32_t h = pack_f16(lo, hi);
+        qb[m][0][s][w] = h;
+        if constexpr (kF32) qb[m][P - 1][s][w] = rest_f16(h, lo, hi);
       }
     }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      fac[m][c] = __shfl_sync(0xffffffffu, row_fac, (2 * t + c) * 4);
+      lim[m][c] = __shfl_sync(0xffffffffu, row_lim, (2 * t + c) * 4);
+    }
+    lim_min = min(lim_min, row_lim);
   }
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
 
-  float acc[MT][NT][4];
-  float mref[MT][2], lsum[MT][2];
+  float acc[NR][MT][4];  // (element g or g + 8 of the m16 tile, row 2 t or 2 t + 1)
+  float mref[NR][2], lsum[NR][2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int m = 0; m < NR; ++m) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < MT; ++j)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.0f;
     mref[m][0] = mref[m][1] = -INFINITY;
     lsum[m][0] = lsum[m][1] = 0.0f;
   }
+  __syncthreads();  // the barriers are there
 
   bool ok = true;
-  for (int step = warp, it = 0; step < n_steps; step += kWarps, ++it) {
-    const int s = it % S;
-    if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], (it / S) & 1))) {
+  // Row g of the 8 keys j is key 8 j + kap: with this order neither the loads of
+  // keys nor those of values (four rows at once) meet a bank twice.
+  const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;
+  for (int i = warp / kGroup, it = 0; i < n_stages; i += kGroups, ++it) {
+    const int s = i % S;
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], (i / S) & 1))) {
       ok = false;
-      for (int j = it; j < it + S && warp + j * kWarps < n_steps; ++j)  // copies under way
-        tc::mbar_wait(&full[j % S], (j / S) & 1);
+      for (int j = i; j < i + S && j < n_stages; ++j)  // copies under way
+        tc::mbar_wait(&full[j % S], (j / S) & 1, tc::kWaitCycles / 16);
       break;
     }
-    const uint8_t* kc = ring + s * step_bytes<D>();
-    const uint8_t* vc = kc + kStep * CB;
-    const uint8_t* ks = kc + 2 * kStep * CB;
-    const uint8_t* vs = ks + kStep * SB;
-    const int k0 = k_begin + step * kStep;
-
-    // ---- logits: n8 tile j holds keys 8 j + kappa(column)
-    float sc[MT][4][4];
-    const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int key = 8 * j + kap;
-      uint32_t kw[E / 8];
-      uint32_t s0, s1;  // float16 scale pairs of the thread's groups
-      if constexpr (D == 128) {
-        const uint4 w = *reinterpret_cast<const uint4*>(kc + key * CB + t * 16);
-        kw[0] = w.x, kw[1] = w.y, kw[2] = w.z, kw[3] = w.w;
-        uint32_t sb = *reinterpret_cast<const uint16_t*>(ks + key * SB + t * 2);
-        const uint32_t vb = *reinterpret_cast<const uint16_t*>(vs + key * SB + t * 2);
-        if (((vb & 0x7F7Fu) + 0x0101u) & 0x8080u) sb = 0x7F7Fu;
-        const uint32_t h = kv4::e4m3x2_to_f16x2(sb);
-        s0 = __byte_perm(h, h, 0x1010);
-        s1 = __byte_perm(h, h, 0x3232);
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(kc + key * CB + t * 8);
-        kw[0] = w.x, kw[1] = w.y;
-        uint32_t sb = ks[key * SB + t];
-        if (kv4::scale_is_nan(vs[key * SB + t])) sb = 0x7Fu;
-        const uint32_t h = kv4::e4m3x2_to_f16x2(sb);
-        s0 = s1 = __byte_perm(h, h, 0x1010);
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[m][j][c] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < E / 8; ++w) {
-        uint32_t p[4];
-        kv4::e2m1x8_to_f16x2(kw[w], p);
-        const uint32_t sg = D == 128 && w >= 2 ? s1 : s0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) p[x] = hmul2(p[x], sg);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int q = 0; q < P; ++q) {
-            mma16816(sc[m][j], qa[m][q][2 * w], p[0], p[1]);
-            mma16816(sc[m][j], qa[m][q][2 * w + 1], p[2], p[3]);
-          }
-      }
-    }
-
-    // ---- running maximum and probabilities
-    uint32_t pa[MT][P][2][4];  // A fragments of the two k16 steps over keys
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (k0 + kStep > lim_min) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = k0 + 8 * j + ((c & 1) ? 4 + (t ^ 1) : t);
-            if (key >= lim[m][c >> 1]) sc[m][j][c] = -INFINITY;
-          }
-      }
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c >> 1] = fmaxf(mx[c >> 1], sc[m][j][c]);
-      bool move = false;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * fac[m][h];
-        move |= mx[h] > mref[m][h] + kSlack;
-      }
-      if (__any_sync(0xffffffffu, move)) {
-        float al[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float to = fmaxf(mref[m][h], mx[h]);
-          al[h] = to == mref[m][h] ? 1.0f : tc::ex2(mref[m][h] - to);
-          mref[m][h] = to;
-          lsum[m][h] *= al[h];
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[m][j][c] *= al[c >> 1];
-      }
-      const float off[2] = {kShift - (mref[m][0] == -INFINITY ? 0.0f : mref[m][0]),
-                            kShift - (mref[m][1] == -INFINITY ? 0.0f : mref[m][1])};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float p[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          p[c] = tc::ex2(fmaf(sc[m][j][c], fac[m][c >> 1], off[c >> 1]));
-          lsum[m][c >> 1] += p[c];
-        }
-        const int u = j >> 1, w = (j & 1) * 2;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x = pack_f16(p[2 * h], p[2 * h + 1]);
-          pa[m][0][u][w + h] = x;
-          if constexpr (kF32) pa[m][P - 1][u][w + h] = rest_f16(x, p[2 * h], p[2 * h + 1]);
-        }
-      }
-    }
-
-    // ---- values: column g of n8 tile j is element g D/8 + j
+    const int k0 = k_begin + i * kStage + (warp % kGroup) * kStep;
+    const uint8_t* kc = smem + s * stage_bytes<D>() + (warp % kGroup) * (kStep * CB);
+    const uint8_t* vc = kc + kStage * CB;
+    const uint8_t* ks = smem + s * stage_bytes<D>() + 2 * kStage * CB + (warp % kGroup) * (kStep * SB);
+    const uint8_t* vs = ks + kStage * SB;
     const int left = k_end - k0;
+    if (left > 0) {
+      // ---- scales of the values: keys 16 u + {t, 4 + (t^1), 8 + t, 12 + (t^1)}, the
+      // group of the thread's elements
+      uint32_t vsc[2][2];
+      {
+        const uint8_t* p0 = vs + t * SB + (D == 128 ? g : g >> 1);
+        const uint8_t* p1 = vs + (4 + (t ^ 1)) * SB + (D == 128 ? g : g >> 1);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      constexpr int W = D / 64;  // words of D/8 codes
-      uint32_t w[4][W];
-      uint32_t sb[4];
-      const int key[4] = {16 * u + t, 16 * u + 4 + (t ^ 1), 16 * u + 8 + t, 16 * u + 12 + (t ^ 1)};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if constexpr (D == 128) {
-          const uint2 v = *reinterpret_cast<const uint2*>(vc + key[x] * CB + g * 8);
-          w[x][0] = v.x, w[x][W - 1] = v.y;
-          sb[x] = vs[key[x] * SB + g];
-        } else {
-          w[x][0] = *reinterpret_cast<const uint32_t*>(vc + key[x] * CB + g * 4);
-          sb[x] = vs[key[x] * SB + (g >> 1)];
+        for (int u = 0; u < 2; ++u) {
+          vsc[u][0] = p0[16 * u * SB] + 256u * p1[16 * u * SB];
+          vsc[u][1] = p0[(16 * u + 8) * SB] + 256u * p1[(16 * u + 8) * SB];
         }
       }
-      const uint32_t sab = value_scales(sb[0], sb[1], key[0] < left, key[1] < left);
-      const uint32_t scd = value_scales(sb[2], sb[3], key[2] < left, key[3] < left);
+      if (left < kStep) {  // rows behind the last key: not used, whatever they hold
 #pragma unroll
-      for (int x = 0; x < W; ++x) {
-        uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd elements of the word
-        kv4::e2m1x8_to_f16x2((w[0][x] & 0x0F0F0F0Fu) | ((w[1][x] << 4) & 0xF0F0F0F0u), e0);
-        kv4::e2m1x8_to_f16x2(((w[0][x] >> 4) & 0x0F0F0F0Fu) | (w[1][x] & 0xF0F0F0F0u), o0);
-        kv4::e2m1x8_to_f16x2((w[2][x] & 0x0F0F0F0Fu) | ((w[3][x] << 4) & 0xF0F0F0F0u), e1);
-        kv4::e2m1x8_to_f16x2(((w[2][x] >> 4) & 0x0F0F0F0Fu) | (w[3][x] & 0xF0F0F0F0u), o1);
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint32_t be0 = hmul2(e0[y], sab), be1 = hmul2(e1[y], scd);
-          const uint32_t bo0 = hmul2(o0[y], sab), bo1 = hmul2(o1[y], scd);
+          for (int w = 0; w < 2; ++w) {
+            if (16 * u + 8 * w + t >= left) vsc[u][w] &= 0xFF00u;
+            if (16 * u + 8 * w + 4 + (t ^ 1) >= left) vsc[u][w] &= 0x00FFu;
+          }
+      }
+      const bool any_nan = __any_sync(
+          0xffffffffu, (nan_bits(vsc[0][0]) | nan_bits(vsc[0][1]) | nan_bits(vsc[1][0]) |
+                        nan_bits(vsc[1][1])) != 0);
+
+      // ---- logits: m16 tile u holds keys 16 u + kap (rows g) and 16 u + 8 + kap
+      float sc[NR][2][4];
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+      for (int u = 0; u < 2; ++u) {
+        uint32_t kw[2][E / 8];
+        uint32_t s0[2], s1[2];  // float16 scale pairs of the thread's groups
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = 16 * u + 8 * h;
+          if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(kc + kap * CB + t * 16 + key * CB);
+            kw[h][0] = w.x, kw[h][1] = w.y, kw[h][2] = w.z, kw[h][3] = w.w;
+            const uint32_t x = kv4::e4m3x2_to_f16x2(
+                *reinterpret_cast<const uint16_t*>(ks + kap * SB + t * 2 + key * SB));
+            s0[h] = __byte_perm(x, x, 0x1010);
+            s1[h] = __byte_perm(x, x, 0x3232);
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(kc + kap * CB + t * 8 + key * CB);
+            kw[h][0] = w.x, kw[h][1] = w.y;
+            const uint32_t x = kv4::e4m3x2_to_f16x2(ks[kap * SB + t + key * SB]);
+            s0[h] = s1[h] = __byte_perm(x, x, 0x1010);
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < E / 8; ++w) {
+          uint32_t p[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            kv4::e2m1x8_to_f16x2(kw[h][w], p[h]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) p[h][x] = hmul2(p[h][x], D == 128 && w >= 2 ? s1[h] : s0[h]);
+          }
+          const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+          const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+#pragma unroll
+          for (int m = 0; m < NR; ++m)
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-              mma16816(acc[m][8 * x + 2 * y], pa[m][q][u], be0, be1);
-              mma16816(acc[m][8 * x + 2 * y + 1], pa[m][q][u], bo0, bo1);
+              if (w == 0 && q == 0)
+                mma_first(sc[m][u], a0, qb[m][q][0][0], qb[m][q][0][1]);
+              else
+                mma_add(sc[m][u], a0, qb[m][q][2 * w][0], qb[m][q][2 * w][1]);
+              mma_add(sc[m][u], a1, qb[m][q][2 * w + 1][0], qb[m][q][2 * w + 1][1]);
             }
+        }
+      }
+      if (any_nan) {  // a NaN among a key's values goes with its logits, and reads as zero
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // the lanes of one t hold the groups of two keys
+            uint32_t bad = nan_bits(vsc[u][h]);
+            vsc[u][h] &= ~((bad >> 7) * 0xFFu);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+            // key kap of the eight: lane t = g / 2 (even g) or (g / 2) of the odd ones
+            bad = __shfl_sync(0xffffffffu, bad, g >> 1) & ((g & 1) ? 0x8000u : 0x80u);
+#pragma unroll
+            for (int m = 0; m < NR; ++m)
+              if (bad) sc[m][u][2 * h] = sc[m][u][2 * h + 1] = __int_as_float(0x7fffffff);
+          }
+      }
+
+      // ---- running maximum and probabilities
+      uint32_t pb[NR][P][2][2];  // B fragments of the two k16 steps over keys
+#pragma unroll
+      for (int m = 0; m < NR; ++m) {
+        if (k0 + kStep > lim_min) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (k0 + 16 * u + 8 * (c >> 1) + kap >= lim[m][c & 1]) sc[m][u][c] = -INFINITY;
+        }
+        float mx[2];
+        bool move = false;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mx[c] = fmaxf(tc::fmax3(sc[m][0][c], sc[m][0][2 + c], sc[m][1][c]), sc[m][1][2 + c]);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
+          mx[c] *= fac[m][c];
+          move |= mx[c] > mref[m][c] + kSlack;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          float al[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float to = fmaxf(mref[m][c], mx[c]);
+            al[c] = to == mref[m][c] ? 1.0f : tc::ex2(mref[m][c] - to);
+            mref[m][c] = to;
+            lsum[m][c] *= al[c];
+          }
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[m][j][c] *= al[c & 1];
+        }
+        const float off[2] = {kShift - (mref[m][0] == -INFINITY ? 0.0f : mref[m][0]),
+                              kShift - (mref[m][1] == -INFINITY ? 0.0f : mref[m][1])};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float p[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              p[c] = tc::ex2(fmaf(sc[m][u][2 * h + c], fac[m][c], off[c]));
+              lsum[m][c] += p[c];
+            }
+            // (keys on the lanes' rows, query rows on the columns) to the B operand
+            const uint32_t x = pack_f16(p[0], p[1]);
+            pb[m][0][u][h] = transpose8x8(x);
+            if constexpr (kF32) pb[m][P - 1][u][h] = transpose8x8(rest_f16(x, p[0], p[1]));
+          }
+      }
+
+      // ---- values are the A operand: rows g and g + 8 of m16 tile j are elements
+      // g D/8 + 2 j and + 2 j + 1
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        constexpr int VW = D / 64;  // words of D/8 codes
+        uint32_t w[4][VW];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int key = 16 * u + 4 * x + ((x & 1) ? t ^ 1 : t);
+          if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2*>(vc + key * CB + g * 8);
+            w[x][0] = v.x, w[x][VW - 1] = v.y;
+          } else {
+            w[x][0] = *reinterpret_cast<const uint32_t*>(vc + key * CB + g * 4);
+          }
+        }
+        const uint32_t sab = kv4::e4m3x2_to_f16x2(vsc[u][0]), scd = kv4::e4m3x2_to_f16x2(vsc[u][1]);
+#pragma unroll
+        for (int x = 0; x < VW; ++x) {
+          uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd elements of the word
+          kv4::e2m1x8_to_f16x2((w[0][x] & 0x0F0F0F0Fu) | ((w[1][x] << 4) & 0xF0F0F0F0u), e0);
+          kv4::e2m1x8_to_f16x2(((w[0][x] >> 4) & 0x0F0F0F0Fu) | (w[1][x] & 0xF0F0F0F0u), o0);
+          kv4::e2m1x8_to_f16x2((w[2][x] & 0x0F0F0F0Fu) | ((w[3][x] << 4) & 0xF0F0F0F0u), e1);
+          kv4::e2m1x8_to_f16x2(((w[2][x] >> 4) & 0x0F0F0F0Fu) | (w[3][x] & 0xF0F0F0F0u), o1);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t av[4] = {hmul2(e0[y], sab), hmul2(o0[y], sab), hmul2(e1[y], scd),
+                                    hmul2(o1[y], scd)};
+#pragma unroll
+            for (int m = 0; m < NR; ++m)
+#pragma unroll
+              for (int q = 0; q < P; ++q)
+                mma_add(acc[m][4 * x + y], av, pb[m][q][u][0], pb[m][q][u][1]);
+          }
         }
       }
     }
     __syncwarp();  // every lane has read the stage
-    if (lane == 0 && step + S * kWarps < n_steps) fetch(step + S * kWarps);
+    if (lane == 0) {
+      tc::mbar_arrive(&empty[s]);
+      // One warp of the group in turn refills the stage that the group finished
+      // before this one.
+      const int done = i - kGroups;
+      if (it % kGroup == warp % kGroup && done >= 0 && done + S < n_stages) {
+        if (tc::mbar_wait(&empty[done % S], (done / S) & 1))
+          fetch(done + S);
+        else
+          ok = false;
+      }
+    }
   }
+  if (!ok) atomicExch(a.err, 1);
+  __syncthreads();
 
   // ---- join the warps: each leaves (maximum, sum) and its outputs per row
-  if (!ok) atomicExch(a.err, 1);
-  float* mine = reinterpret_cast<float*>(ring);
-  __syncwarp();
+  constexpr int RS = D + 4;  // floats of a row: D outputs, maximum, sum
+  float* mine = reinterpret_cast<float*>(smem + warp * warp_result_bytes<D, NR>());
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < NR; ++m)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float l = lsum[m][h];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int row = m * 16 + h * 8 + g;
-      if (t == 0) {
-        mine[row * 2] = mref[m][h];
-        mine[row * 2 + 1] = l;
+    for (int c = 0; c < 2; ++c) {
+      float l = lsum[m][c];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      float* row = mine + (m * 8 + 2 * t + c) * RS;
+      if (g == 0) {
+        row[D] = mref[m][c];
+        row[D + 1] = l;
       }
-      // thread t holds elements t D/4 .. of the row: columns 2t (first half)
-      // and 2t + 1
-      float* o = mine + MT * 32 + row * D + t * E;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        o[j] = acc[m][j][2 * h];
-        o[NT + j] = acc[m][j][2 * h + 1];
-      }
+      for (int j = 0; j < MT; ++j)
+        *reinterpret_cast<float2*>(row + g * (D / 8) + 2 * j) =
+            make_float2(acc[m][j][c], acc[m][j][2 + c]);
     }
   __syncthreads();
   const float* all = reinterpret_cast<const float*>(smem);
-  constexpr int WB = warp_bytes<D, MT>() / 4;
-  for (int i = threadIdx.x; i < MT * 16 * (D / 4); i += kThreads) {
+  constexpr int WB = warp_result_bytes<D, NR>() / 4;
+  for (int i = threadIdx.x; i < NR * 8 * (D / 4); i += kThreads) {
     const int row = i / (D / 4), c = (i % (D / 4)) * 4;
     const int r = r_base + row;
     if (r >= a.R) break;
+    const float* at_row = all + row * RS;
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, all[w * WB + row * 2]);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, at_row[w * WB + D]);
     const float ref = M == -INFINITY ? 0.0f : M;
     float L = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = tc::ex2(all[w * WB + row * 2] - ref);
-      L += f * all[w * WB + row * 2 + 1];
-      const float4 x = *reinterpret_cast<const float4*>(all + w * WB + MT * 32 + row * D + c);
+      const float f = tc::ex2(at_row[w * WB + D] - ref);
+      L += f * at_row[w * WB + D + 1];
+      const float4 x = *reinterpret_cast<const float4*>(at_row + w * WB + c);
       o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
     }
     if (a.n_split == 1) {
@@ -421,9 +492,9 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
 
 // Join the shares of a row: one block per row, its warps over the shares.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
-  __shared__ float4 part[kWarps][32];
-  __shared__ float part_l[kWarps];
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnArgs a) {
+  __shared__ float4 part[kJoinWarps][32];
+  __shared__ float part_l[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x;  // unit * R + r
   const int unit = (int)(row / a.R), r = (int)(row % a.R);
@@ -443,7 +514,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   const bool col = lane < D / 4;
 #pragma unroll 4
-  for (int s = warp; s < ns; s += kWarps) {
+  for (int s = warp; s < ns; s += kJoinWarps) {
     const float2 x = ml[s];
     const float f = tc::ex2(x.x - ref);
     L += f * x.y;
@@ -458,7 +529,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnArgs a) {
   if (warp == 0 && col) {
     L = part_l[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
+    for (int w = 1; w < kJoinWarps; ++w) {
       const float4 v = part[w][lane];
       o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
       L += part_l[w];
@@ -490,10 +561,10 @@ Shares choose_split(int64_t units, int max_len, int64_t slots, int least, int64_
   return s;
 }
 
-template <typename T, int D, int MT>
-cudaError_t run(AttnArgs a, int N, cudaStream_t s) {
-  constexpr int smem = smem_bytes<D, MT>();
-  cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<T, D, MT>,
+template <typename T, int D, int NR>
+cudaError_t run(const AttnArgs& a, int N, cudaStream_t s) {
+  constexpr int smem = smem_bytes<D, NR>();
+  cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<T, D, NR>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (int64_t)N * a.Hkv * a.n_rb * a.n_split;
@@ -506,7 +577,7 @@ cudaError_t run(AttnArgs a, int N, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<T, D, MT>, a);
+  e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<T, D, NR>, a);
   if (e != cudaSuccess) return e;
   add_launches(1);
   return cudaGetLastError();
@@ -519,7 +590,7 @@ cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -529,8 +600,8 @@ cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// The tensor-core kernel takes over where its 256-row blocks are worth filling.
-bool use_tc(bool bf16, int R) { return bf16 && R > 64; }
+// The tcgen05 kernel takes over where the rows do not fit one pass of this one.
+bool use_tc(bool bf16, int R) { return bf16 && R > 16; }
 
 struct Layout {
   int rows_blk, n_rb, n_split, chunk;
@@ -540,11 +611,11 @@ Layout layout(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d) {
   Layout l;
   const int R = Hq / Hkv * Lq;
   const bool tc = use_tc(bf16, R);
-  l.rows_blk = tc ? kTcRows : bf16 && R > 16 ? 32 : 16;
+  l.rows_blk = tc ? kTcRows : R > 8 ? 16 : 8;
   l.n_rb = (int)ceil_div(R, l.rows_blk);
   const int64_t units = (int64_t)N * Hkv * l.n_rb;
   const Shares sh = tc ? choose_split(units, max_len, sm_count(), 512, 1)
-                       : choose_split(units, max_len, 3ll * sm_count(), 256, 3);
+                       : choose_split(units, max_len, 2ll * sm_count(), 256, 3);
   l.n_split = sh.n_split;
   l.chunk = sh.chunk;
   const size_t parts = sh.n_most > 1 ? (size_t)N * Hkv * R * sh.n_most : 0;
@@ -557,14 +628,12 @@ Layout layout(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d) {
 template <int D>
 cudaError_t run_all(const AttnArgs& a, bool bf16, int N, cudaStream_t s) {
   cudaError_t e;
-  if (!bf16)
-    e = run<float, D, 1>(a, N, s);
-  else if (a.rows_blk == kTcRows)
+  if (a.rows_blk == kTcRows)
     e = launch_attn_tc(a, N, D, s);
-  else if (a.rows_blk == 16)
-    e = run<__nv_bfloat16, D, 1>(a, N, s);
+  else if (a.rows_blk == 8)
+    e = bf16 ? run<__nv_bfloat16, D, 1>(a, N, s) : run<float, D, 1>(a, N, s);
   else
-    e = run<__nv_bfloat16, D, 2>(a, N, s);
+    e = bf16 ? run<__nv_bfloat16, D, 2>(a, N, s) : run<float, D, 2>(a, N, s);
   if (e != cudaSuccess || a.n_split == 1) return e;
   return bf16 ? join<__nv_bfloat16, D>(a, N, s) : join<float, D>(a, N, s);
 }
