@@ -60,16 +60,14 @@ template <int D, int NR> constexpr int smem_bytes() {
 // c = a b (+ c): m16n8k16, float16 operands, float32 sums.
 __device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma_add(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -269,48 +267,50 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
 
       // ---- logits: m16 tile u holds keys 16 u + kap (rows g) and 16 u + 8 + kap
       float sc[NR][2][4];
+      {
+        uint32_t kw[4][E / 8];
+        uint32_t s0[4], s1[4];  // float16 scale pairs of the thread's groups
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t kw[2][E / 8];
-        uint32_t s0[2], s1[2];  // float16 scale pairs of the thread's groups
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = 16 * u + 8 * h;
+        for (int h = 0; h < 4; ++h) {
           if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(kc + kap * CB + t * 16 + key * CB);
+            const uint4 w = *reinterpret_cast<const uint4*>(kc + kap * CB + t * 16 + 8 * h * CB);
             kw[h][0] = w.x, kw[h][1] = w.y, kw[h][2] = w.z, kw[h][3] = w.w;
             const uint32_t x = kv4::e4m3x2_to_f16x2(
-                *reinterpret_cast<const uint16_t*>(ks + kap * SB + t * 2 + key * SB));
+                *reinterpret_cast<const uint16_t*>(ks + kap * SB + t * 2 + 8 * h * SB));
             s0[h] = __byte_perm(x, x, 0x1010);
             s1[h] = __byte_perm(x, x, 0x3232);
           } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(kc + kap * CB + t * 8 + key * CB);
+            const uint2 w = *reinterpret_cast<const uint2*>(kc + kap * CB + t * 8 + 8 * h * CB);
             kw[h][0] = w.x, kw[h][1] = w.y;
-            const uint32_t x = kv4::e4m3x2_to_f16x2(ks[kap * SB + t + key * SB]);
+            const uint32_t x = kv4::e4m3x2_to_f16x2(ks[kap * SB + t + 8 * h * SB]);
             s0[h] = s1[h] = __byte_perm(x, x, 0x1010);
           }
         }
 #pragma unroll
         for (int w = 0; w < E / 8; ++w) {
-          uint32_t p[2][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            kv4::e2m1x8_to_f16x2(kw[h][w], p[h]);
+          for (int u = 0; u < 2; ++u) {
+            uint32_t p[2][4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) p[h][x] = hmul2(p[h][x], D == 128 && w >= 2 ? s1[h] : s0[h]);
-          }
-          const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
-          const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+            for (int h = 0; h < 2; ++h) {
+              kv4::e2m1x8_to_f16x2(kw[2 * u + h][w], p[h]);
 #pragma unroll
-          for (int m = 0; m < NR; ++m)
-#pragma unroll
-            for (int q = 0; q < P; ++q) {
-              if (w == 0 && q == 0)
-                mma_first(sc[m][u], a0, qb[m][q][0][0], qb[m][q][0][1]);
-              else
-                mma_add(sc[m][u], a0, qb[m][q][2 * w][0], qb[m][q][2 * w][1]);
-              mma_add(sc[m][u], a1, qb[m][q][2 * w + 1][0], qb[m][q][2 * w + 1][1]);
+              for (int x = 0; x < 4; ++x)
+                p[h][x] = hmul2(p[h][x], D == 128 && w >= 2 ? s1[2 * u + h] : s0[2 * u + h]);
             }
+            const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+            const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+#pragma unroll
+            for (int m = 0; m < NR; ++m)
+#pragma unroll
+              for (int q = 0; q < P; ++q) {
+                if (w == 0 && q == 0)
+                  mma_first(sc[m][u], a0, qb[m][q][0][0], qb[m][q][0][1]);
+                else
+                  mma_add(sc[m][u], a0, qb[m][q][2 * w][0], qb[m][q][2 * w][1]);
+                mma_add(sc[m][u], a1, qb[m][q][2 * w + 1][0], qb[m][q][2 * w + 1][1]);
+              }
+          }
         }
       }
       if (any_nan) {  // a NaN among a key's values goes with its logits, and reads as zero
