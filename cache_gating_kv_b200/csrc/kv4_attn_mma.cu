@@ -38,6 +38,7 @@ namespace fc {
 
 namespace {
 constexpr int kStep = 32;      // keys of a warp's step
+constexpr int kU = kStep / 16; // m16 tiles of a step
 constexpr int kGroup = 4;      // warps that work on one stage
 constexpr int kWarps = 8;      // two groups, taking stages in turn
 constexpr int kGroups = kWarps / kGroup;
@@ -46,7 +47,10 @@ constexpr int kStage = kGroup * kStep;
 constexpr int kJoinWarps = 4;
 
 template <int D> constexpr int stage_bytes() { return kStage * (D + D / 8); }
-template <int D> constexpr int stages() { return D == 128 ? 5 : 8; }
+// A multiple of the groups, so that a stage's slot always belongs to one group: its
+// warps then wait for every phase of the slot's barrier, and a wait for one phase
+// cannot be answered by the phase two before it.
+template <int D> constexpr int stages() { return D == 128 ? 6 : 8; }
 // Outputs of a row at the end, with two numbers beside them and an odd stride.
 template <int D, int NR> constexpr int warp_result_bytes() { return NR * 8 * (D + 4) * 4; }
 template <int D, int NR> constexpr int ring_bytes() {
@@ -113,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   constexpr int E = D / 4;          // elements of d that a thread holds of a key
   constexpr int CB = D / 2, SB = D / 16;
   constexpr int S = stages<D>();
+  static_assert(S % kGroups == 0, "a slot belongs to one group");
   constexpr int P = kF32 ? 2 : 1;   // float16 terms of queries and probabilities
   constexpr float kShift = kF32 ? 14.0f : 5.0f;
   constexpr float kSlack = kF32 ? 0.0f : 8.0f;
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes<D, NR>());
-  uint64_t* empty = full + S;
+  uint32_t* readers = reinterpret_cast<uint32_t*>(full + S);  // warps done with a stage
 
   int b = blockIdx.x;
   const int split = b % a.n_split;
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], kGroup);
+      readers[s] = 0;
     }
     tc::fence_barrier_init();
   }
@@ -240,63 +245,63 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     const uint8_t* vs = ks + kStage * SB;
     const int left = k_end - k0;
     if (left > 0) {
-      // ---- scales of the values: keys 16 u + {t, 4 + (t^1), 8 + t, 12 + (t^1)}, the
-      // group of the thread's elements
-      uint32_t vsc[2][2];
+      // ---- scales of the values: bytes x of vsc[u] are keys 16 u + 4 x + (t, t^1, t,
+      // t^1), the group of the thread's elements
+      uint32_t vsc[kU];
       {
         const uint8_t* p0 = vs + t * SB + (D == 128 ? g : g >> 1);
         const uint8_t* p1 = vs + (4 + (t ^ 1)) * SB + (D == 128 ? g : g >> 1);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          vsc[u][0] = p0[16 * u * SB] + 256u * p1[16 * u * SB];
-          vsc[u][1] = p0[(16 * u + 8) * SB] + 256u * p1[(16 * u + 8) * SB];
-        }
+        for (int u = 0; u < kU; ++u)
+          vsc[u] = p0[16 * u * SB] + 0x100u * p1[16 * u * SB] + 0x10000u * p0[(16 * u + 8) * SB] +
+                   0x1000000u * p1[(16 * u + 8) * SB];
       }
       if (left < kStep) {  // rows behind the last key: not used, whatever they hold
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (16 * u + 8 * w + t >= left) vsc[u][w] &= 0xFF00u;
-            if (16 * u + 8 * w + 4 + (t ^ 1) >= left) vsc[u][w] &= 0x00FFu;
-          }
+          for (int x = 0; x < 4; ++x)
+            if (16 * u + 4 * x + ((x & 1) ? t ^ 1 : t) >= left) vsc[u] &= ~(0xFFu << (8 * x));
       }
-      const bool any_nan = __any_sync(
-          0xffffffffu, (nan_bits(vsc[0][0]) | nan_bits(vsc[0][1]) | nan_bits(vsc[1][0]) |
-                        nan_bits(vsc[1][1])) != 0);
+      uint32_t nans = 0;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) nans |= nan_bits(vsc[u]);
+      const bool any_nan = __any_sync(0xffffffffu, nans != 0);
 
       // ---- logits: m16 tile u holds keys 16 u + kap (rows g) and 16 u + 8 + kap
-      float sc[NR][2][4];
-      {
+      float sc[NR][kU][4];
+#pragma unroll
+      for (int v = 0; v < kU; v += 2) {  // two tiles at a time
         uint32_t kw[4][E / 8];
         uint32_t s0[4], s1[4];  // float16 scale pairs of the thread's groups
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
+          const int key = 16 * v + 8 * h;
           if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(kc + kap * CB + t * 16 + 8 * h * CB);
+            const uint4 w = *reinterpret_cast<const uint4*>(kc + kap * CB + t * 16 + key * CB);
             kw[h][0] = w.x, kw[h][1] = w.y, kw[h][2] = w.z, kw[h][3] = w.w;
             const uint32_t x = kv4::e4m3x2_to_f16x2(
-                *reinterpret_cast<const uint16_t*>(ks + kap * SB + t * 2 + 8 * h * SB));
+                *reinterpret_cast<const uint16_t*>(ks + kap * SB + t * 2 + key * SB));
             s0[h] = __byte_perm(x, x, 0x1010);
             s1[h] = __byte_perm(x, x, 0x3232);
           } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(kc + kap * CB + t * 8 + 8 * h * CB);
+            const uint2 w = *reinterpret_cast<const uint2*>(kc + kap * CB + t * 8 + key * CB);
             kw[h][0] = w.x, kw[h][1] = w.y;
-            const uint32_t x = kv4::e4m3x2_to_f16x2(ks[kap * SB + t + 8 * h * SB]);
+            const uint32_t x = kv4::e4m3x2_to_f16x2(ks[kap * SB + t + key * SB]);
             s0[h] = s1[h] = __byte_perm(x, x, 0x1010);
           }
         }
 #pragma unroll
         for (int w = 0; w < E / 8; ++w) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int y = 0; y < 2; ++y) {
             uint32_t p[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              kv4::e2m1x8_to_f16x2(kw[2 * u + h][w], p[h]);
+              kv4::e2m1x8_to_f16x2(kw[2 * y + h][w], p[h]);
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                p[h][x] = hmul2(p[h][x], D == 128 && w >= 2 ? s1[2 * u + h] : s0[2 * u + h]);
+                p[h][x] = hmul2(p[h][x], D == 128 && w >= 2 ? s1[2 * y + h] : s0[2 * y + h]);
             }
             const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
             const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
@@ -305,39 +310,39 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
 #pragma unroll
               for (int q = 0; q < P; ++q) {
                 if (w == 0 && q == 0)
-                  mma_first(sc[m][u], a0, qb[m][q][0][0], qb[m][q][0][1]);
+                  mma_first(sc[m][v + y], a0, qb[m][q][0][0], qb[m][q][0][1]);
                 else
-                  mma_add(sc[m][u], a0, qb[m][q][2 * w][0], qb[m][q][2 * w][1]);
-                mma_add(sc[m][u], a1, qb[m][q][2 * w + 1][0], qb[m][q][2 * w + 1][1]);
+                  mma_add(sc[m][v + y], a0, qb[m][q][2 * w][0], qb[m][q][2 * w][1]);
+                mma_add(sc[m][v + y], a1, qb[m][q][2 * w + 1][0], qb[m][q][2 * w + 1][1]);
               }
           }
         }
       }
       if (any_nan) {  // a NaN among a key's values goes with its logits, and reads as zero
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kU; ++u) {
+          // the lanes of one t hold the groups of four keys
+          uint32_t bad = nan_bits(vsc[u]);
+          vsc[u] &= ~((bad >> 7) * 0xFFu);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // the lanes of one t hold the groups of two keys
-            uint32_t bad = nan_bits(vsc[u][h]);
-            vsc[u][h] &= ~((bad >> 7) * 0xFFu);
+          for (int o = 4; o < 32; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+          // the thread's own keys, 16 u + kap and + 8: bytes of lane g / 2
+          bad = __shfl_sync(0xffffffffu, bad, g >> 1) >> ((g & 1) ? 8 : 0);
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-            // key kap of the eight: lane t = g / 2 (even g) or (g / 2) of the odd ones
-            bad = __shfl_sync(0xffffffffu, bad, g >> 1) & ((g & 1) ? 0x8000u : 0x80u);
-#pragma unroll
-            for (int m = 0; m < NR; ++m)
-              if (bad) sc[m][u][2 * h] = sc[m][u][2 * h + 1] = __int_as_float(0x7fffffff);
+          for (int m = 0; m < NR; ++m) {
+            if (bad & 0x80u) sc[m][u][0] = sc[m][u][1] = __int_as_float(0x7fffffff);
+            if (bad & 0x800000u) sc[m][u][2] = sc[m][u][3] = __int_as_float(0x7fffffff);
           }
+        }
       }
 
       // ---- running maximum and probabilities
-      uint32_t pb[NR][P][2][2];  // B fragments of the two k16 steps over keys
+      uint32_t pb[NR][P][kU][2];  // B fragments of the k16 steps over keys
 #pragma unroll
       for (int m = 0; m < NR; ++m) {
         if (k0 + kStep > lim_min) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < kU; ++u)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               if (k0 + 16 * u + 8 * (c >> 1) + kap >= lim[m][c & 1]) sc[m][u][c] = -INFINITY;
@@ -346,7 +351,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
         bool move = false;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          mx[c] = fmaxf(tc::fmax3(sc[m][0][c], sc[m][0][2 + c], sc[m][1][c]), sc[m][1][2 + c]);
+          mx[c] = fmaxf(sc[m][0][c], sc[m][0][2 + c]);
+#pragma unroll
+          for (int u = 1; u < kU; ++u) mx[c] = tc::fmax3(mx[c], sc[m][u][c], sc[m][u][2 + c]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
           mx[c] *= fac[m][c];
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
         const float off[2] = {kShift - (mref[m][0] == -INFINITY ? 0.0f : mref[m][0]),
                               kShift - (mref[m][1] == -INFINITY ? 0.0f : mref[m][1])};
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float p[2];
@@ -388,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
       // ---- values are the A operand: rows g and g + 8 of m16 tile j are elements
       // g D/8 + 2 j and + 2 j + 1
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kU; ++u) {
         constexpr int VW = D / 64;  // words of D/8 codes
         uint32_t w[4][VW];
 #pragma unroll
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
             w[x][0] = *reinterpret_cast<const uint32_t*>(vc + key * CB + g * 4);
           }
         }
-        const uint32_t sab = kv4::e4m3x2_to_f16x2(vsc[u][0]), scd = kv4::e4m3x2_to_f16x2(vsc[u][1]);
+        const uint32_t sab = kv4::e4m3x2_to_f16x2(vsc[u]), scd = kv4::e4m3x2_to_f16x2(vsc[u] >> 16);
 #pragma unroll
         for (int x = 0; x < VW; ++x) {
           uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd elements of the word
@@ -423,16 +430,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
       }
     }
     __syncwarp();  // every lane has read the stage
-    if (lane == 0) {
-      tc::mbar_arrive(&empty[s]);
-      // One warp of the group in turn refills the stage that the group finished
-      // before this one.
-      const int done = i - kGroups;
-      if (it % kGroup == warp % kGroup && done >= 0 && done + S < n_stages) {
-        if (tc::mbar_wait(&empty[done % S], (done / S) & 1))
-          fetch(done + S);
-        else
-          ok = false;
+    if (lane == 0) {  // the group's last warp refills it
+      __threadfence_block();
+      if (atomicAdd(&readers[s], 1u) % kGroup == kGroup - 1 && i + S < n_stages) {
+        __threadfence_block();
+        fetch(i + S);
       }
     }
   }
