@@ -230,95 +230,107 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   // Row g of the 8 keys j is key 8 j + kap: with this order neither the loads of
   // keys nor those of values (four rows at once) meet a bank twice.
   const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;
-  for (int i = warp / kGroup, it = 0; i < n_stages; i += kGroups, ++it) {
-    const int s = i % S;
-    if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], (i / S) & 1))) {
-      ok = false;
-      for (int j = i; j < i + S && j < n_stages; ++j)  // copies under way
-        tc::mbar_wait(&full[j % S], (j / S) & 1, tc::kWaitCycles / 16);
-      break;
-    }
-    const int k0 = k_begin + i * kStage + (warp % kGroup) * kStep;
-    const uint8_t* kc = smem + s * stage_bytes<D>() + (warp % kGroup) * (kStep * CB);
-    const uint8_t* vc = kc + kStage * CB;
-    const uint8_t* ks = smem + s * stage_bytes<D>() + 2 * kStage * CB + (warp % kGroup) * (kStep * SB);
-    const uint8_t* vs = ks + kStage * SB;
-    const int left = k_end - k0;
-    if (left > 0) {
-      // ---- scales of the values: bytes x of vsc[u] are keys 16 u + 4 x + (t, t^1, t,
-      // t^1), the group of the thread's elements
-      uint32_t vsc[kU];
-      {
-        const uint8_t* p0 = vs + t * SB + (D == 128 ? g : g >> 1);
-        const uint8_t* p1 = vs + (4 + (t ^ 1)) * SB + (D == 128 ? g : g >> 1);
+  const int w_off = (warp % kGroup) * kStep;  // the warp's keys of a stage
+
+  // Logits of the warp's keys of stage i: m16 tile u holds keys 16 u + kap (rows g)
+  // and 16 u + 8 + kap.
+  float sc[NR][kU][4];
+  auto logits = [&](int i) {
+    const uint8_t* st = smem + (i % S) * stage_bytes<D>();
+    const uint8_t* kc = st + (w_off + kap) * CB + t * (CB / 4);
+    const uint8_t* ks = st + 2 * kStage * CB + (w_off + kap) * SB + t * (SB / 4);
+    uint32_t kw[2 * kU][E / 8];
+    uint32_t s0[2 * kU], s1[2 * kU];  // float16 scale pairs of the thread's groups
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-          vsc[u] = p0[16 * u * SB] + 0x100u * p1[16 * u * SB] + 0x10000u * p0[(16 * u + 8) * SB] +
-                   0x1000000u * p1[(16 * u + 8) * SB];
+    for (int h = 0; h < 2 * kU; ++h) {
+      if constexpr (D == 128) {
+        const uint4 w = *reinterpret_cast<const uint4*>(kc + 8 * h * CB);
+        kw[h][0] = w.x, kw[h][1] = w.y, kw[h][2] = w.z, kw[h][3] = w.w;
+        const uint32_t x =
+            kv4::e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + 8 * h * SB));
+        s0[h] = __byte_perm(x, x, 0x1010);
+        s1[h] = __byte_perm(x, x, 0x3232);
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(kc + 8 * h * CB);
+        kw[h][0] = w.x, kw[h][1] = w.y;
+        const uint32_t x = kv4::e4m3x2_to_f16x2(ks[8 * h * SB]);
+        s0[h] = s1[h] = __byte_perm(x, x, 0x1010);
       }
-      if (left < kStep) {  // rows behind the last key: not used, whatever they hold
+    }
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
+    for (int w = 0; w < E / 8; ++w) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        uint32_t p[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          kv4::e2m1x8_to_f16x2(kw[2 * u + h][w], p[h]);
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            if (16 * u + 4 * x + ((x & 1) ? t ^ 1 : t) >= left) vsc[u] &= ~(0xFFu << (8 * x));
+            p[h][x] = hmul2(p[h][x], D == 128 && w >= 2 ? s1[2 * u + h] : s0[2 * u + h]);
+        }
+        const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+        const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+#pragma unroll
+        for (int m = 0; m < NR; ++m)
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            if (w == 0 && q == 0)
+              mma_first(sc[m][u], a0, qb[m][q][0][0], qb[m][q][0][1]);
+            else
+              mma_add(sc[m][u], a0, qb[m][q][2 * w][0], qb[m][q][2 * w][1]);
+            mma_add(sc[m][u], a1, qb[m][q][2 * w + 1][0], qb[m][q][2 * w + 1][1]);
+          }
       }
+    }
+  };
+
+  // Probabilities of stage i from its logits, and the scales of its values: byte x
+  // of vsc[u] is key 16 u + 4 x + (t, t^1, t, t^1), the group of the thread's
+  // elements.
+  uint32_t pb[NR][P][kU][2];  // B fragments of the k16 steps over keys
+  uint32_t vsc[kU];
+  auto softmax = [&](int i) {
+    const int k0 = k_begin + i * kStage + w_off;
+    const uint8_t* vs = smem + (i % S) * stage_bytes<D>() + kStage * (2 * CB + SB) + w_off * SB +
+                        (D == 128 ? g : g >> 1);
+    const uint8_t *p0 = vs + t * SB, *p1 = vs + (4 + (t ^ 1)) * SB;
+    uint32_t odd = 0;  // something to look after: NaN scales, a row to rescale
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      vsc[u] = p0[16 * u * SB] + 0x100u * p1[16 * u * SB] + 0x10000u * p0[(16 * u + 8) * SB] +
+               0x1000000u * p1[(16 * u + 8) * SB];
+      odd |= nan_bits(vsc[u]);
+    }
+    if (k0 + kStep > lim_min) {  // keys that a row does not see, rows behind the last key
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+#pragma unroll
+        for (int m = 0; m < NR; ++m)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (k0 + 16 * u + 8 * (c >> 1) + kap >= lim[m][c & 1]) sc[m][u][c] = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (k0 + 16 * u + 4 * x + ((x & 1) ? t ^ 1 : t) >= k_end) vsc[u] &= ~(0xFFu << (8 * x));
+      }
+    }
+    float mx[NR][2];  // of the thread's own keys
+#pragma unroll
+    for (int m = 0; m < NR; ++m)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mx[m][c] = fmaxf(sc[m][0][c], sc[m][0][2 + c]);
+#pragma unroll
+        for (int u = 1; u < kU; ++u) mx[m][c] = tc::fmax3(mx[m][c], sc[m][u][c], sc[m][u][2 + c]);
+        odd |= mx[m][c] * fac[m][c] > mref[m][c] + kSlack ? 1u : 0u;
+      }
+    if (__any_sync(0xffffffffu, odd != 0)) {
       uint32_t nans = 0;
 #pragma unroll
       for (int u = 0; u < kU; ++u) nans |= nan_bits(vsc[u]);
-      const bool any_nan = __any_sync(0xffffffffu, nans != 0);
-
-      // ---- logits: m16 tile u holds keys 16 u + kap (rows g) and 16 u + 8 + kap
-      float sc[NR][kU][4];
-#pragma unroll
-      for (int v = 0; v < kU; v += 2) {  // two tiles at a time
-        uint32_t kw[4][E / 8];
-        uint32_t s0[4], s1[4];  // float16 scale pairs of the thread's groups
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int key = 16 * v + 8 * h;
-          if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(kc + kap * CB + t * 16 + key * CB);
-            kw[h][0] = w.x, kw[h][1] = w.y, kw[h][2] = w.z, kw[h][3] = w.w;
-            const uint32_t x = kv4::e4m3x2_to_f16x2(
-                *reinterpret_cast<const uint16_t*>(ks + kap * SB + t * 2 + key * SB));
-            s0[h] = __byte_perm(x, x, 0x1010);
-            s1[h] = __byte_perm(x, x, 0x3232);
-          } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(kc + kap * CB + t * 8 + key * CB);
-            kw[h][0] = w.x, kw[h][1] = w.y;
-            const uint32_t x = kv4::e4m3x2_to_f16x2(ks[kap * SB + t + key * SB]);
-            s0[h] = s1[h] = __byte_perm(x, x, 0x1010);
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < E / 8; ++w) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint32_t p[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              kv4::e2m1x8_to_f16x2(kw[2 * y + h][w], p[h]);
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                p[h][x] = hmul2(p[h][x], D == 128 && w >= 2 ? s1[2 * y + h] : s0[2 * y + h]);
-            }
-            const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
-            const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
-#pragma unroll
-            for (int m = 0; m < NR; ++m)
-#pragma unroll
-              for (int q = 0; q < P; ++q) {
-                if (w == 0 && q == 0)
-                  mma_first(sc[m][v + y], a0, qb[m][q][0][0], qb[m][q][0][1]);
-                else
-                  mma_add(sc[m][v + y], a0, qb[m][q][2 * w][0], qb[m][q][2 * w][1]);
-                mma_add(sc[m][v + y], a1, qb[m][q][2 * w + 1][0], qb[m][q][2 * w + 1][1]);
-              }
-          }
-        }
-      }
-      if (any_nan) {  // a NaN among a key's values goes with its logits, and reads as zero
+      if (__any_sync(0xffffffffu, nans != 0)) {
+        // a NaN among a key's values goes with its logits, and reads as zero
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           // the lanes of one t hold the groups of four keys
@@ -330,113 +342,131 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
           bad = __shfl_sync(0xffffffffu, bad, g >> 1) >> ((g & 1) ? 8 : 0);
 #pragma unroll
           for (int m = 0; m < NR; ++m) {
-            if (bad & 0x80u) sc[m][u][0] = sc[m][u][1] = __int_as_float(0x7fffffff);
-            if (bad & 0x800000u) sc[m][u][2] = sc[m][u][3] = __int_as_float(0x7fffffff);
-          }
-        }
-      }
-
-      // ---- running maximum and probabilities
-      uint32_t pb[NR][P][kU][2];  // B fragments of the k16 steps over keys
-#pragma unroll
-      for (int m = 0; m < NR; ++m) {
-        if (k0 + kStep > lim_min) {
-#pragma unroll
-          for (int u = 0; u < kU; ++u)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (k0 + 16 * u + 8 * (c >> 1) + kap >= lim[m][c & 1]) sc[m][u][c] = -INFINITY;
+              if (bad & (c < 2 ? 0x80u : 0x800000u) &&
+                  k0 + 16 * u + 8 * (c >> 1) + kap < lim[m][c & 1])
+                sc[m][u][c] = __int_as_float(0x7fffffff);
+          }
         }
-        float mx[2];
-        bool move = false;
+      }
+      // the row's largest, and everything of the row so far relative to it
+#pragma unroll
+      for (int m = 0; m < NR; ++m) {
+        float al[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          mx[c] = fmaxf(sc[m][0][c], sc[m][0][2 + c]);
+          float top = mx[m][c];
 #pragma unroll
-          for (int u = 1; u < kU; ++u) mx[c] = tc::fmax3(mx[c], sc[m][u][c], sc[m][u][2 + c]);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
-          mx[c] *= fac[m][c];
-          move |= mx[c] > mref[m][c] + kSlack;
+          for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          top *= fac[m][c];
+          const float to = top > mref[m][c] + kSlack ? top : mref[m][c];
+          al[c] = to == mref[m][c] ? 1.0f : tc::ex2(mref[m][c] - to);
+          mref[m][c] = to;
+          lsum[m][c] *= al[c];
         }
-        if (__any_sync(0xffffffffu, move)) {
-          float al[2];
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[m][j][c] *= al[c & 1];
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < NR; ++m) {
+      const float off[2] = {kShift - (mref[m][0] == -INFINITY ? 0.0f : mref[m][0]),
+                            kShift - (mref[m][1] == -INFINITY ? 0.0f : mref[m][1])};
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float p[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float to = fmaxf(mref[m][c], mx[c]);
-            al[c] = to == mref[m][c] ? 1.0f : tc::ex2(mref[m][c] - to);
-            mref[m][c] = to;
-            lsum[m][c] *= al[c];
+            p[c] = tc::ex2(fmaf(sc[m][u][2 * h + c], fac[m][c], off[c]));
+            lsum[m][c] += p[c];
           }
-#pragma unroll
-          for (int j = 0; j < MT; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[m][j][c] *= al[c & 1];
+          // (keys on the lanes' rows, query rows on the columns) to the B operand
+          const uint32_t x = pack_f16(p[0], p[1]);
+          pb[m][0][u][h] = transpose8x8(x);
+          if constexpr (kF32) pb[m][P - 1][u][h] = transpose8x8(rest_f16(x, p[0], p[1]));
         }
-        const float off[2] = {kShift - (mref[m][0] == -INFINITY ? 0.0f : mref[m][0]),
-                              kShift - (mref[m][1] == -INFINITY ? 0.0f : mref[m][1])};
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float p[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              p[c] = tc::ex2(fmaf(sc[m][u][2 * h + c], fac[m][c], off[c]));
-              lsum[m][c] += p[c];
-            }
-            // (keys on the lanes' rows, query rows on the columns) to the B operand
-            const uint32_t x = pack_f16(p[0], p[1]);
-            pb[m][0][u][h] = transpose8x8(x);
-            if constexpr (kF32) pb[m][P - 1][u][h] = transpose8x8(rest_f16(x, p[0], p[1]));
-          }
-      }
+    }
+  };
 
-      // ---- values are the A operand: rows g and g + 8 of m16 tile j are elements
-      // g D/8 + 2 j and + 2 j + 1
+  // Values of stage i are the A operand: rows g and g + 8 of m16 tile j are elements
+  // g D/8 + 2 j and + 2 j + 1.
+  auto values = [&](int i) {
+    const uint8_t* vc = smem + (i % S) * stage_bytes<D>() + kStage * CB + w_off * CB + g * (CB / 8);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        constexpr int VW = D / 64;  // words of D/8 codes
-        uint32_t w[4][VW];
+    for (int u = 0; u < kU; ++u) {
+      constexpr int VW = D / 64;  // words of D/8 codes
+      uint32_t w[4][VW];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = 16 * u + 4 * x + ((x & 1) ? t ^ 1 : t);
-          if constexpr (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2*>(vc + key * CB + g * 8);
-            w[x][0] = v.x, w[x][VW - 1] = v.y;
-          } else {
-            w[x][0] = *reinterpret_cast<const uint32_t*>(vc + key * CB + g * 4);
-          }
+      for (int x = 0; x < 4; ++x) {
+        const uint8_t* at = vc + (16 * u + 4 * x + ((x & 1) ? t ^ 1 : t)) * CB;
+        if constexpr (D == 128) {
+          const uint2 v = *reinterpret_cast<const uint2*>(at);
+          w[x][0] = v.x, w[x][VW - 1] = v.y;
+        } else {
+          w[x][0] = *reinterpret_cast<const uint32_t*>(at);
         }
-        const uint32_t sab = kv4::e4m3x2_to_f16x2(vsc[u]), scd = kv4::e4m3x2_to_f16x2(vsc[u] >> 16);
+      }
+      const uint32_t sab = kv4::e4m3x2_to_f16x2(vsc[u]), scd = kv4::e4m3x2_to_f16x2(vsc[u] >> 16);
 #pragma unroll
-        for (int x = 0; x < VW; ++x) {
-          uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd elements of the word
-          kv4::e2m1x8_to_f16x2((w[0][x] & 0x0F0F0F0Fu) | ((w[1][x] << 4) & 0xF0F0F0F0u), e0);
-          kv4::e2m1x8_to_f16x2(((w[0][x] >> 4) & 0x0F0F0F0Fu) | (w[1][x] & 0xF0F0F0F0u), o0);
-          kv4::e2m1x8_to_f16x2((w[2][x] & 0x0F0F0F0Fu) | ((w[3][x] << 4) & 0xF0F0F0F0u), e1);
-          kv4::e2m1x8_to_f16x2(((w[2][x] >> 4) & 0x0F0F0F0Fu) | (w[3][x] & 0xF0F0F0F0u), o1);
+      for (int x = 0; x < VW; ++x) {
+        uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd elements of the word
+        kv4::e2m1x8_to_f16x2((w[0][x] & 0x0F0F0F0Fu) | ((w[1][x] << 4) & 0xF0F0F0F0u), e0);
+        kv4::e2m1x8_to_f16x2(((w[0][x] >> 4) & 0x0F0F0F0Fu) | (w[1][x] & 0xF0F0F0F0u), o0);
+        kv4::e2m1x8_to_f16x2((w[2][x] & 0x0F0F0F0Fu) | ((w[3][x] << 4) & 0xF0F0F0F0u), e1);
+        kv4::e2m1x8_to_f16x2(((w[2][x] >> 4) & 0x0F0F0F0Fu) | (w[3][x] & 0xF0F0F0F0u), o1);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t av[4] = {hmul2(e0[y], sab), hmul2(o0[y], sab), hmul2(e1[y], scd),
-                                    hmul2(o1[y], scd)};
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t av[4] = {hmul2(e0[y], sab), hmul2(o0[y], sab), hmul2(e1[y], scd),
+                                  hmul2(o1[y], scd)};
 #pragma unroll
-            for (int m = 0; m < NR; ++m)
+          for (int m = 0; m < NR; ++m)
 #pragma unroll
-              for (int q = 0; q < P; ++q)
-                mma_add(acc[m][4 * x + y], av, pb[m][q][u][0], pb[m][q][u][1]);
-          }
+            for (int q = 0; q < P; ++q)
+              mma_add(acc[m][4 * x + y], av, pb[m][q][u][0], pb[m][q][u][1]);
         }
       }
     }
+  };
+  auto arrived = [&](int i) {
+    const bool in = __all_sync(0xffffffffu, tc::mbar_wait(&full[i % S], (i / S) & 1));
+    if (!in) {
+      ok = false;
+      for (int j = i; j < i + S && j < n_stages; ++j)  // copies under way
+        tc::mbar_wait(&full[j % S], (j / S) & 1, tc::kWaitCycles / 16);
+    }
+    return in;
+  };
+  auto release = [&](int i) {
     __syncwarp();  // every lane has read the stage
     if (lane == 0) {  // the group's last warp refills it
       __threadfence_block();
-      if (atomicAdd(&readers[s], 1u) % kGroup == kGroup - 1 && i + S < n_stages) {
+      if (atomicAdd(&readers[i % S], 1u) % kGroup == kGroup - 1 && i + S < n_stages) {
         __threadfence_block();
         fetch(i + S);
       }
     }
+  };
+
+  // Stages of the warp that hold keys for it, one ahead: the values of a stage and the
+  // logits of the next are independent work for one instruction stream.
+  const int n_mine = k_end - k_begin > w_off ? (k_end - k_begin - w_off + kStage - 1) / kStage : 0;
+  int i = warp / kGroup;
+  if (i < n_mine && arrived(i)) {
+    logits(i);
+    softmax(i);
+    for (int nx = i + kGroups; nx < n_mine; i = nx, nx += kGroups) {
+      if (!arrived(nx)) break;
+      logits(nx);
+      values(i);
+      release(i);
+      softmax(nx);
+    }
+    if (ok) values(i);
   }
   if (!ok) atomicExch(a.err, 1);
   __syncthreads();
