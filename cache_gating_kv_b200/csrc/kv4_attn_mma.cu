@@ -44,7 +44,7 @@ constexpr int kWarps = 8;      // two groups, taking stages in turn
 constexpr int kGroups = kWarps / kGroup;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStage = kGroup * kStep;
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
 
 template <int D> constexpr int stage_bytes() { return kStage * (D + D / 8); }
 // A multiple of the groups, so that a stage's slot always belongs to one group: its
@@ -84,6 +84,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+__device__ __forceinline__ uint32_t both_low(uint32_t x) {
+  const __half2 r = __low2half2(reinterpret_cast<const __half2&>(x));
+  return reinterpret_cast<const uint32_t&>(r);
+}
+__device__ __forceinline__ uint32_t both_high(uint32_t x) {
+  const __half2 r = __high2half2(reinterpret_cast<const __half2&>(x));
+  return reinterpret_cast<const uint32_t&>(r);
+}
 // What float16 rounding left of (lo, hi).
 __device__ __forceinline__ uint32_t rest_f16(uint32_t h, float lo, float hi) {
   const float2 f = __half22float2(reinterpret_cast<const __half2&>(h));
@@ -125,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes<D, NR>());
-  uint32_t* readers = reinterpret_cast<uint32_t*>(full + S);  // warps done with a stage
+  uint64_t* empty = full + S;
 
   int b = blockIdx.x;
   const int split = b % a.n_split;
@@ -137,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       tc::mbar_init(&full[s], 1);
-      readers[s] = 0;
+      tc::mbar_init(&empty[s], kGroup);
     }
     tc::fence_barrier_init();
   }
@@ -248,13 +256,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
         kw[h][0] = w.x, kw[h][1] = w.y, kw[h][2] = w.z, kw[h][3] = w.w;
         const uint32_t x =
             kv4::e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + 8 * h * SB));
-        s0[h] = __byte_perm(x, x, 0x1010);
-        s1[h] = __byte_perm(x, x, 0x3232);
+        s0[h] = both_low(x);
+        s1[h] = both_high(x);
       } else {
         const uint2 w = *reinterpret_cast<const uint2*>(kc + 8 * h * CB);
         kw[h][0] = w.x, kw[h][1] = w.y;
         const uint32_t x = kv4::e4m3x2_to_f16x2(ks[8 * h * SB]);
-        s0[h] = s1[h] = __byte_perm(x, x, 0x1010);
+        s0[h] = s1[h] = both_low(x);
       }
     }
 #pragma unroll
@@ -443,12 +451,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   };
   auto release = [&](int i) {
     __syncwarp();  // every lane has read the stage
-    if (lane == 0) {  // the group's last warp refills it
-      __threadfence_block();
-      if (atomicAdd(&readers[i % S], 1u) % kGroup == kGroup - 1 && i + S < n_stages) {
-        __threadfence_block();
+    if (lane == 0) tc::mbar_arrive(&empty[i % S]);
+  };
+  // One warp of the group, in turn, refills the stage that the group has released; it
+  // comes to that a softmax later than its own release, so the others have too.
+  auto refill = [&](int i) {
+    if (lane == 0 && i + S < n_stages && (i / kGroups) % kGroup == warp % kGroup) {
+      if (tc::mbar_wait(&empty[i % S], (i / S) & 1))
         fetch(i + S);
-      }
+      else
+        ok = false;
     }
   };
 
@@ -465,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
       values(i);
       release(i);
       softmax(nx);
+      refill(i);
     }
     if (ok) values(i);
   }
@@ -522,21 +535,36 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   }
 }
 
-// Join the shares of a row: one block per row, its warps over the shares.
+// Join the shares of a row: one block per row, its warps over the shares.  What this
+// costs is latency, so everything that does not wait for the shares comes before
+// the wait for them, and a warp's first loads do not wait for the reference.
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnArgs a) {
+  constexpr int kAhead = 5;
   __shared__ float4 part[kJoinWarps][32];
   __shared__ float part_l[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int64_t row = blockIdx.x;  // unit * R + r
   const int unit = (int)(row / a.R), r = (int)(row % a.R);
   const int n = unit / a.Hkv, hk = unit % a.Hkv;
-  grid_dep_wait();
-  grid_dep_launch();
+  // Lengths are older than the kernel that this one depends on, which waited for
+  // them itself before it let this one start.
   const int len = seq_len(a, n);
   const int k_top = block_keys(a, len, r / a.rows_blk * a.rows_blk, a.rows_blk);
   const int ns = (k_top + a.chunk - 1) / a.chunk;
+  const bool col = lane < D / 4;
   const float2* ml = a.part_ml + row * a.n_split;
+  const float4* po = reinterpret_cast<const float4*>(a.part_o + row * a.n_split * D) + lane;
+  grid_dep_wait();
+  grid_dep_launch();
+  float2 x[kAhead];
+  float4 v[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int s = warp + k * nw;
+    x[k] = s < ns ? ml[s] : make_float2(-INFINITY, 0.0f);
+    v[k] = s < ns && col ? po[(int64_t)s * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   float M = -INFINITY;
   for (int s = lane; s < ns; s += 32) M = fmaxf(M, ml[s].x);
 #pragma unroll
@@ -544,26 +572,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
   const float ref = M == -INFINITY ? 0.0f : M;
   float L = 0.0f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  const bool col = lane < D / 4;
+  auto add = [&](float2 xs, float4 vs) {
+    const float f = tc::ex2(xs.x - ref);
+    L += f * xs.y;
+    o.x += f * vs.x, o.y += f * vs.y, o.z += f * vs.z, o.w += f * vs.w;
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (warp + k * nw < ns) add(x[k], v[k]);
 #pragma unroll 4
-  for (int s = warp; s < ns; s += kJoinWarps) {
-    const float2 x = ml[s];
-    const float f = tc::ex2(x.x - ref);
-    L += f * x.y;
-    if (col) {
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + (row * a.n_split + s) * D + lane * 4);
-      o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
-    }
-  }
+  for (int s = warp + kAhead * nw; s < ns; s += nw)
+    add(ml[s], col ? po[(int64_t)s * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f));
   part[warp][lane] = o;
   if (lane == 0) part_l[warp] = L;
   __syncthreads();
   if (warp == 0 && col) {
-    L = part_l[0];
-#pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) {
-      const float4 v = part[w][lane];
-      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    for (int w = 1; w < nw; ++w) {
+      const float4 y = part[w][lane];
+      o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
       L += part_l[w];
     }
     write_row<T>(a, n, hk, r, lane * 4, o, M, L);
@@ -622,7 +648,7 @@ cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows);
-  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.blockDim = dim3(32 * (a.n_split < kJoinWarps ? a.n_split : kJoinWarps));
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
