@@ -16,14 +16,18 @@ struct AttnArgs {
   const int32_t* lens;
   Strides qs, os;
   const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
-  int Hkv, G, R, Lq, max_len, cap;  // R = G * Lq rows of a key head
-  int rows_blk, n_rb, n_split, chunk;
+  int N, Hkv, G, R, Lq, max_len, cap;  // R = G * Lq rows of a key head
+  int rows_blk, n_rb;                  // query rows of a block, row blocks of a key head
+  int n_split, chunk;
+  bool stream;                         // shares of equal work (StreamShare)
+  int blocks;                          // of the grid that computes
   bool causal;
   float scale_log2;  // scale * 2^k_exp * log2 e
   float out_scale;   // 2^v_exp
   int* err;
-  float2* part_ml;  // [N Hkv R][n_split] (log2 reference, sum)
-  float* part_o;    // [N Hkv R][n_split][d]
+  float2* part_ml;  // [N Hkv R][n_split] (log2 reference, sum); stream: [blocks][2][rows_blk]
+  float* part_o;    // [N Hkv R][n_split][d]; stream: [blocks][2][rows_blk][d]
+  int2* part_of;    // stream: [N Hkv][n_rb] (first block, blocks) of a unit
 };
 
 __device__ __forceinline__ int seq_len(const AttnArgs& a, int n) {
@@ -56,6 +60,135 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
       : "memory");
 }
+
+// Shares of equal work.  A unit is one key head of one sequence with one block of
+// query rows; its work is its key stages (of kStageKeys) and kUnitCost more for what
+// a unit costs whatever its length (loading its queries, filling and emptying the
+// pipeline, joining the warps).  Units lie one behind the other in the order
+// (sequence, row block, key head), the fixed cost first, and block c of C takes the
+// work from floor(T c / C) to floor(T (c + 1) / C) of all T, whatever the lengths are:
+// it ends the unit that an earlier block began, takes whole ones, and begins one.  A
+// unit whose stages several blocks share leaves one part for each, in slot 1 of the
+// block with its first stage and slot 0 of the others, and a second kernel joins
+// them.  The lengths are on the device, so every block adds up the work itself.
+constexpr int kStageKeys = 128;
+constexpr int kUnitCost = 3;
+
+__device__ __forceinline__ int entry_stages(const AttnArgs& a, int e) {
+  const int n = a.n_rb == 1 ? e : e / a.n_rb;
+  const int rb = e - n * a.n_rb;
+  const int keys = block_keys(a, seq_len(a, n), rb * a.rows_blk, a.rows_blk);
+  return (keys + kStageKeys - 1) / kStageKeys;
+}
+// Work of one key head of an entry (sequence, row block).
+__device__ __forceinline__ int entry_work(const AttnArgs& a, int e) {
+  const int s = entry_stages(a, e);
+  return s > 0 ? s + kUnitCost : 0;
+}
+// x / y for x >= 0, y > 0, mostly small.
+__device__ __forceinline__ int64_t div_small(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return (int64_t)((uint32_t)x / (uint32_t)y);
+  return x / y;
+}
+
+// A piece of a share: stages [s_begin, s_end) of n_unit of a unit.
+struct Piece {
+  int n, hk, rb, n_unit, s_begin, s_end;
+  int n_parts;  // blocks that share the unit, where this one has its first stage
+};
+
+// A block's share, in shared memory (in registers it would stay through the loops
+// over stages).  begin() is called by the whole block, next() by one thread.
+template <int kThreads>
+struct StreamShare {
+  int64_t warp_sum[kThreads / 32];
+  int64_t total, pos, end;  // all work, the share's
+  int64_t start;            // the work before entry e
+  int C, e;                 // blocks, entry (sequence, row block) at pos
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, int least) {
+    const int E = a.N * a.n_rb;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (E + kThreads - 1) / kThreads;
+    const int e0 = threadIdx.x * per, e1 = min(E, e0 + per);
+    int64_t own = 0;
+    for (int i = e0; i < e1; ++i) own += entry_work(a, i);
+    own *= a.Hkv;
+    int64_t upto = own;  // inclusive
+    if (E > 1) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+    }
+    int64_t all = upto;
+    if (E > per * 32) {  // over more than the first warp
+      if (lane == 31) warp_sum[warp] = upto;
+      __syncthreads();
+      all = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) upto += warp_sum[w];
+        all += warp_sum[w];
+      }
+    } else if (E > 1) {
+      all = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (E > per * 32 || warp == 0) {
+      const int64_t most = all / least;  // a constant
+      const int blocks = most < 1 ? 1 : most < (int64_t)gridDim.x ? (int)most : (int)gridDim.x;
+      const int c = blockIdx.x;
+      const int64_t lo = c < blocks ? div_small(all * c, blocks) : 0;
+      const int64_t hi = c < blocks ? div_small(all * (c + 1), blocks) : 0;
+      if (lo >= hi) {
+        if (threadIdx.x == 0) pos = end = 0;
+      } else if (upto - own <= lo && lo < upto) {
+        int64_t at = upto - own;
+        int i = e0;
+        for (;; ++i) {
+          const int64_t w = (int64_t)entry_work(a, i) * a.Hkv;
+          if (lo < at + w) break;
+          at += w;
+        }
+        total = all;
+        pos = lo;
+        end = hi;
+        start = at;
+        C = blocks;
+        e = i;
+      }
+    }
+    __syncthreads();
+  }
+
+  // The next piece with stages; false at the end of the share.
+  __device__ __forceinline__ bool next(const AttnArgs& a, Piece& p) {
+    while (pos < end) {
+      int w;
+      while ((w = entry_work(a, e)) == 0) ++e;
+      p.n = a.n_rb == 1 ? e : e / a.n_rb;
+      p.rb = e - p.n * a.n_rb;
+      p.n_unit = w - kUnitCost;
+      p.hk = (int)div_small(pos - start, w);
+      const int64_t unit0 = start + (int64_t)p.hk * w;
+      const int from = (int)(pos - unit0), to = (int)min((int64_t)w, from + (end - pos));
+      p.s_begin = max(0, from - kUnitCost);
+      p.s_end = max(0, to - kUnitCost);
+      // the block with the unit's last stage: the largest c with T c / C <= it
+      p.n_parts = 1;
+      if (p.s_begin == 0 && p.s_end > 0 && p.s_end < p.n_unit)
+        p.n_parts = (int)div_small((unit0 + w) * C - 1, total) - (int)blockIdx.x + 1;
+      pos += to - from;
+      if (to == w && p.hk == a.Hkv - 1) {
+        start = pos;
+        ++e;
+      }
+      if (p.s_end > p.s_begin) return true;
+    }
+    return false;
+  }
+};
 
 // Four outputs of row r from their weighted sums o, the row's log2 reference
 // and its sum L of 2^(x - ref).

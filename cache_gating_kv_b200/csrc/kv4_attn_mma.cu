@@ -44,7 +44,9 @@ constexpr int kWarps = 8;      // two groups, taking stages in turn
 constexpr int kGroups = kWarps / kGroup;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStage = kGroup * kStep;
+static_assert(kStage == kStageKeys, "stages are the unit of the shares");
 constexpr int kJoinWarps = 8;
+constexpr int kLeastStages = 2;  // of a block's share
 
 template <int D> constexpr int stage_bytes() { return kStage * (D + D / 8); }
 // A multiple of the groups, so that a stage's slot always belongs to one group: its
@@ -135,12 +137,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes<D, NR>());
   uint64_t* empty = full + S;
 
-  int b = blockIdx.x;
-  const int split = b % a.n_split;
-  b /= a.n_split;
-  const int rb = b % a.n_rb;
-  const int unit = b / a.n_rb;  // n * Hkv + key head
-  const int n = unit / a.Hkv, hk = unit % a.Hkv;
+  __shared__ StreamShare<kThreads> share;
+  __shared__ Piece piece;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -152,18 +150,34 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   grid_dep_wait();
   grid_dep_launch();
 
-  const int len = seq_len(a, n);
-  const int r_base = rb * 8 * NR;
-  const int k_top = block_keys(a, len, r_base, 8 * NR);
-  const int k_begin = split * a.chunk;
-  const int k_end = min(k_top, k_begin + a.chunk);
-  if (a.n_split > 1 && k_begin >= k_end) return;  // the join does not look for it
-  const int n_stages = k_begin < k_end ? (k_end - k_begin + kStage - 1) / kStage : 0;
+  // The block's share: one unit, or a run of stages over units.
+  if (a.stream) share.begin(a, kLeastStages);
+  bool ok = true;
+  int base = 0;  // stages of the units before: slots and phases go on
+  for (;;) {
+  if (threadIdx.x == 0) {
+    if (a.stream) {
+      if (!share.next(a, piece)) piece.n_unit = -1;
+    } else {
+      const int unit = blockIdx.x / a.n_rb;
+      piece.n = unit / a.Hkv;
+      piece.hk = unit % a.Hkv;
+      piece.rb = blockIdx.x % a.n_rb;
+      piece.s_begin = 0;
+      piece.s_end = piece.n_unit = entry_stages(a, piece.n * a.n_rb + piece.rb);
+    }
+  }
+  __syncthreads();
+  if (piece.n_unit < 0) return;
+  const int len = seq_len(a, piece.n);
+  const int r_base = piece.rb * 8 * NR;
+  const int k_begin = piece.s_begin * kStage;
+  const int k_end = min(block_keys(a, len, r_base, 8 * NR), piece.s_end * kStage);
+  const int n_stages = piece.s_end - piece.s_begin;
   const int k_pad = (k_end + 15) & ~15;  // rows are copied in sixteens (cap is a multiple)
 
-  const int64_t head = (int64_t)unit * a.cap;
-  auto fetch = [&](int i) {  // one thread: the copies of stage i
-    const int s = i % S;
+  const int64_t head = (int64_t)(piece.n * a.Hkv + piece.hk) * a.cap;
+  auto fetch = [&](int i, int s) {  // one thread: the copies of stage i into slot s
     const int k0 = k_begin + i * kStage;
     const int rows = min(kStage, k_pad - k0);
     uint8_t* dst = smem + s * stage_bytes<D>();
@@ -173,8 +187,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     bulk_load(dst + 2 * kStage * CB, a.k_scales + (head + k0) * SB, rows * SB, &full[s]);
     bulk_load(dst + kStage * (2 * CB + SB), a.v_scales + (head + k0) * SB, rows * SB, &full[s]);
   };
-  if (threadIdx.x == 0)
-    for (int i = 0; i < S && i < n_stages; ++i) fetch(i);
+  if (threadIdx.x == 0) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // behind the last unit's join
+    for (int i = 0; i < S && i < n_stages; ++i) fetch(i, (base + i) % S);
+    if (a.stream && piece.s_begin == 0)
+      a.part_of[(int64_t)(piece.n * a.Hkv + piece.hk) * a.n_rb + piece.rb] =
+          make_int2(blockIdx.x, piece.n_parts);
+  }
 
   // Queries are the B operand: in k16 step s thread (g, t) holds elements
   // t E + 4 s .. + 3 of row g, times a power of two that brings the row's largest
@@ -187,10 +206,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   for (int m = 0; m < NR; ++m) {
     const int r = r_base + m * 8 + g;
     const bool have = r < a.R;
-    const int i = r / a.G, hq = hk * a.G + r % a.G;
+    const int i = r / a.G, hq = piece.hk * a.G + r % a.G;
     const int row_lim = have ? min(k_end, row_keys(a, len, i)) : k_end;
     float f[E];
-    load_q<T, E>(reinterpret_cast<const T*>(a.q) + n * a.qs.n + hq * a.qs.h + i * a.qs.l + t * E,
+    load_q<T, E>(reinterpret_cast<const T*>(a.q) + piece.n * a.qs.n + hq * a.qs.h + i * a.qs.l + t * E,
                  have, f);
     float top = 0.0f;
 #pragma unroll
@@ -234,7 +253,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   }
   __syncthreads();  // the barriers are there
 
-  bool ok = true;
   // Row g of the 8 keys j is key 8 j + kap: with this order neither the loads of
   // keys nor those of values (four rows at once) meet a bank twice.
   const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;
@@ -243,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   // Logits of the warp's keys of stage i: m16 tile u holds keys 16 u + kap (rows g)
   // and 16 u + 8 + kap.
   float sc[NR][kU][4];
-  auto logits = [&](int i) {
-    const uint8_t* st = smem + (i % S) * stage_bytes<D>();
+  auto logits = [&](int s) {
+    const uint8_t* st = smem + s * stage_bytes<D>();
     const uint8_t* kc = st + (w_off + kap) * CB + t * (CB / 4);
     const uint8_t* ks = st + 2 * kStage * CB + (w_off + kap) * SB + t * (SB / 4);
     uint32_t kw[2 * kU][E / 8];
@@ -298,9 +316,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   // elements.
   uint32_t pb[NR][P][kU][2];  // B fragments of the k16 steps over keys
   uint32_t vsc[kU];
-  auto softmax = [&](int i) {
+  auto softmax = [&](int i, int s) {
     const int k0 = k_begin + i * kStage + w_off;
-    const uint8_t* vs = smem + (i % S) * stage_bytes<D>() + kStage * (2 * CB + SB) + w_off * SB +
+    const uint8_t* vs = smem + s * stage_bytes<D>() + kStage * (2 * CB + SB) + w_off * SB +
                         (D == 128 ? g : g >> 1);
     const uint8_t *p0 = vs + t * SB, *p1 = vs + (4 + (t ^ 1)) * SB;
     uint32_t odd = 0;  // something to look after: NaN scales, a row to rescale
@@ -403,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
 
   // Values of stage i are the A operand: rows g and g + 8 of m16 tile j are elements
   // g D/8 + 2 j and + 2 j + 1.
-  auto values = [&](int i) {
-    const uint8_t* vc = smem + (i % S) * stage_bytes<D>() + kStage * CB + w_off * CB + g * (CB / 8);
+  auto values = [&](int s) {
+    const uint8_t* vc = smem + s * stage_bytes<D>() + kStage * CB + w_off * CB + g * (CB / 8);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       constexpr int VW = D / 64;  // words of D/8 codes
@@ -440,25 +458,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
       }
     }
   };
-  auto arrived = [&](int i) {
-    const bool in = __all_sync(0xffffffffu, tc::mbar_wait(&full[i % S], (i / S) & 1));
+  auto arrived = [&](int i, int s, uint32_t parity) {
+    const bool in = __all_sync(0xffffffffu, tc::mbar_wait(&full[s], parity));
     if (!in) {
       ok = false;
-      for (int j = i; j < i + S && j < n_stages; ++j)  // copies under way
-        tc::mbar_wait(&full[j % S], (j / S) & 1, tc::kWaitCycles / 16);
+      for (int x = base + i; x < base + min(i + S, n_stages); ++x)  // copies under way
+        tc::mbar_wait(&full[x % S], (x / S) & 1, tc::kWaitCycles / 16);
     }
     return in;
   };
-  auto release = [&](int i) {
+  auto release = [&](int s) {
     __syncwarp();  // every lane has read the stage
-    if (lane == 0) tc::mbar_arrive(&empty[i % S]);
+    if (lane == 0) tc::mbar_arrive(&empty[s]);
   };
   // One warp of the group, in turn, refills the stage that the group has released; it
   // comes to that a softmax later than its own release, so the others have too.
-  auto refill = [&](int i) {
+  auto refill = [&](int i, int s, uint32_t parity) {
     if (lane == 0 && i + S < n_stages && (i / kGroups) % kGroup == warp % kGroup) {
-      if (tc::mbar_wait(&empty[i % S], (i / S) & 1))
-        fetch(i + S);
+      if (tc::mbar_wait(&empty[s], parity))
+        fetch(i + S, s);
       else
         ok = false;
     }
@@ -467,20 +485,33 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   // Stages of the warp that hold keys for it, one ahead: the values of a stage and the
   // logits of the next are independent work for one instruction stream.
   const int n_mine = k_end - k_begin > w_off ? (k_end - k_begin - w_off + kStage - 1) / kStage : 0;
-  int i = warp / kGroup;
-  if (i < n_mine && arrived(i)) {
-    logits(i);
-    softmax(i);
-    for (int nx = i + kGroups; nx < n_mine; i = nx, nx += kGroups) {
-      if (!arrived(nx)) break;
-      logits(nx);
-      values(i);
-      release(i);
-      softmax(nx);
-      refill(i);
+  int i = (warp / kGroup + base) % kGroups;  // slots stay with their group
+  int slot = (base + i) % S;
+  uint32_t parity = ((base + i) / S) & 1;
+  if (i < n_mine && arrived(i, slot, parity)) {
+    logits(slot);
+    softmax(i, slot);
+    for (int nx = i + kGroups; nx < n_mine; nx += kGroups) {
+      int to = slot + kGroups;
+      uint32_t to_parity = parity;
+      if (to >= S) {
+        to -= S;
+        to_parity ^= 1;
+      }
+      if (!arrived(nx, to, to_parity)) break;
+      logits(to);
+      values(slot);
+      release(slot);
+      softmax(nx, to);
+      refill(i, slot, parity);
+      i = nx;
+      slot = to;
+      parity = to_parity;
     }
-    if (ok) values(i);
+    if (ok) values(slot);
   }
+  // every phase of a slot has its arrivals
+  for (; i < n_stages; i += kGroups) release((base + i) % S);
   if (!ok) atomicExch(a.err, 1);
   __syncthreads();
 
@@ -525,48 +556,75 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
       const float4 x = *reinterpret_cast<const float4*>(at_row + w * WB + c);
       o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
     }
-    if (a.n_split == 1) {
-      write_row<T>(a, n, hk, r, c, o, M == -INFINITY ? M : M - kShift, L);
+    if (n_stages == piece.n_unit) {
+      write_row<T>(a, piece.n, piece.hk, r, c, o, M == -INFINITY ? M : M - kShift, L);
     } else {
-      const int64_t at = ((int64_t)unit * a.R + r) * a.n_split + split;
+      const int64_t at = ((int64_t)blockIdx.x * 2 + (piece.s_begin == 0 ? 1 : 0)) * (8 * NR) + row;
       if (c == 0) a.part_ml[at] = make_float2(M == -INFINITY ? M : M - kShift, L);
       *reinterpret_cast<float4*>(a.part_o + at * D + c) = o;
     }
   }
+  if (!a.stream) return;
+  base += n_stages;
+  if (__syncthreads_or(!ok)) return;  // the results have been read: the stages are free
+  }
 }
 
-// Join the shares of a row: one block per row, its warps over the shares.  What this
-// costs is latency, so everything that does not wait for the shares comes before
-// the wait for them, and a warp's first loads do not wait for the reference.
-template <typename T, int D>
+// Join the parts of a row.  What this costs is latency, so everything that does not
+// wait for the parts comes before the wait for them, and a warp's first loads do not
+// wait for the reference.  A row of few parts takes one warp (kRowWarps = 1, eight
+// rows to a block), one of many takes a block's eight: with one block to a row of
+// three parts, 1280 rows cost 6 us after the kernel that they wait for, and with
+// warps 3.
+template <typename T, int D, int kRowWarps>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnArgs a) {
   constexpr int kAhead = 5;
   __shared__ float4 part[kJoinWarps][32];
   __shared__ float part_l[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  const int64_t row = blockIdx.x;  // unit * R + r
+  const int lane = threadIdx.x & 31;
+  const int warp = kRowWarps == 1 ? 0 : threadIdx.x >> 5;
+  const int64_t row = kRowWarps == 1 ? (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5)
+                                     : blockIdx.x;  // unit * R + r
+  if (row >= (int64_t)a.N * a.Hkv * a.R) return;
   const int unit = (int)(row / a.R), r = (int)(row % a.R);
   const int n = unit / a.Hkv, hk = unit % a.Hkv;
   // Lengths are older than the kernel that this one depends on, which waited for
   // them itself before it let this one start.
   const int len = seq_len(a, n);
-  const int k_top = block_keys(a, len, r / a.rows_blk * a.rows_blk, a.rows_blk);
-  const int ns = (k_top + a.chunk - 1) / a.chunk;
+  const int rb = r / a.rows_blk;
+  const int k_top = block_keys(a, len, rb * a.rows_blk, a.rows_blk);
+  int ns = (k_top + a.chunk - 1) / a.chunk;
   const bool col = lane < D / 4;
   const float2* ml = a.part_ml + row * a.n_split;
   const float4* po = reinterpret_cast<const float4*>(a.part_o + row * a.n_split * D) + lane;
+  int step = 1;  // rows between parts
   grid_dep_wait();
   grid_dep_launch();
+  if (a.stream) {
+    ns = 0;
+    if (k_top > 0) {
+      const int2 of = a.part_of[(int64_t)unit * a.n_rb + rb];
+      if (of.y == 1) return;  // one block had it all
+      ns = of.y;
+      // slot 1 of the first block, slot 0 of the others: two slots apart but for the
+      // first pair, which lie side by side
+      const int64_t first = ((int64_t)of.x * 2 + 1) * a.rows_blk + r % a.rows_blk;
+      ml = a.part_ml + first;
+      po += (first - row * a.n_split) * (D / 4);
+      step = a.rows_blk;
+    }
+  }
+  auto place = [&](int s) { return (int64_t)(a.stream && s > 0 ? 2 * s - 1 : s) * step; };
   float2 x[kAhead];
   float4 v[kAhead];
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
-    const int s = warp + k * nw;
-    x[k] = s < ns ? ml[s] : make_float2(-INFINITY, 0.0f);
-    v[k] = s < ns && col ? po[(int64_t)s * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int s = warp + k * kRowWarps;
+    x[k] = s < ns ? ml[place(s)] : make_float2(-INFINITY, 0.0f);
+    v[k] = s < ns && col ? po[place(s) * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   float M = -INFINITY;
-  for (int s = lane; s < ns; s += 32) M = fmaxf(M, ml[s].x);
+  for (int s = lane; s < ns; s += 32) M = fmaxf(M, ml[place(s)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ref = M == -INFINITY ? 0.0f : M;
@@ -579,21 +637,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
   };
 #pragma unroll
   for (int k = 0; k < kAhead; ++k)
-    if (warp + k * nw < ns) add(x[k], v[k]);
+    if (warp + k * kRowWarps < ns) add(x[k], v[k]);
 #pragma unroll 4
-  for (int s = warp + kAhead * nw; s < ns; s += nw)
-    add(ml[s], col ? po[(int64_t)s * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f));
-  part[warp][lane] = o;
-  if (lane == 0) part_l[warp] = L;
-  __syncthreads();
-  if (warp == 0 && col) {
-    for (int w = 1; w < nw; ++w) {
+  for (int s = warp + kAhead * kRowWarps; s < ns; s += kRowWarps)
+    add(ml[place(s)], col ? po[place(s) * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f));
+  if constexpr (kRowWarps > 1) {
+    part[warp][lane] = o;
+    if (lane == 0) part_l[warp] = L;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < kRowWarps; ++w) {
       const float4 y = part[w][lane];
       o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
       L += part_l[w];
     }
-    write_row<T>(a, n, hk, r, lane * 4, o, M, L);
   }
+  if (col) write_row<T>(a, n, hk, r, lane * 4, o, M, L);
 }
 
 // Shares of the key axis: enough blocks to fill the SMs, at least `least` keys to
@@ -605,11 +665,10 @@ struct Shares {
   int n_split, chunk;
   int64_t n_most;
 };
-Shares choose_split(int64_t units, int max_len, int64_t slots, int least, int64_t waves) {
+Shares choose_split(int64_t units, int max_len, int64_t slots, int least) {
   Shares s = {1, max_len > 0 ? (int)align_up((size_t)max_len, 128) : 128, 1};
-  if (max_len <= 2 * least || units >= (waves > 1 ? 4 * slots : slots)) return s;
-  // few units: one wave; many: several, so that unlike lengths even out
-  const int64_t want = waves == 1 || units * 4 <= slots ? slots / units : ceil_div(waves * slots, units);
+  if (max_len <= 2 * least || units >= slots) return s;
+  const int64_t want = slots / units;
   if (want <= 1) return s;
   const int64_t c = ceil_div(max_len, want);
   s.chunk = (int)align_up((size_t)(c < least ? least : c), 128);
@@ -625,11 +684,9 @@ cudaError_t run(const AttnArgs& a, int N, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<T, D, NR>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (int64_t)N * a.Hkv * a.n_rb * a.n_split;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)a.blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -644,15 +701,20 @@ cudaError_t run(const AttnArgs& a, int N, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
   const int64_t rows = (int64_t)N * a.Hkv * a.R;
-  if (rows > 0x7fffffffll) return cudaErrorInvalidValue;
+  // parts of a row: of equal shares, about the blocks to a unit
+  const int64_t parts = a.stream ? a.blocks / ((int64_t)N * a.Hkv * a.n_rb) + 2 : a.n_split;
+  const bool one = parts <= 5;
+  const int64_t blocks = one ? ceil_div(rows, kJoinWarps) : rows;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows);
-  cfg.blockDim = dim3(32 * (a.n_split < kJoinWarps ? a.n_split : kJoinWarps));
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, a);
+  const cudaError_t e = one ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, 1>, a)
+                            : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D, kJoinWarps>, a);
   if (e != cudaSuccess) return e;
   add_launches(1);
   return cudaGetLastError();
@@ -662,25 +724,44 @@ cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
 bool use_tc(bool bf16, int R) { return bf16 && R > 16; }
 
 struct Layout {
-  int rows_blk, n_rb, n_split, chunk;
-  size_t ml, o, total;
+  int rows_blk, n_rb, n_split, chunk, blocks;
+  bool stream;
+  size_t of, ml, o, total;
 };
-Layout layout(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d) {
-  Layout l;
+bool layout(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d, Layout& l) {
   const int R = Hq / Hkv * Lq;
   const bool tc = use_tc(bf16, R);
   l.rows_blk = tc ? kTcRows : R > 8 ? 16 : 8;
   l.n_rb = (int)ceil_div(R, l.rows_blk);
   const int64_t units = (int64_t)N * Hkv * l.n_rb;
-  const Shares sh = tc ? choose_split(units, max_len, sm_count(), 512, 1)
-                       : choose_split(units, max_len, 2ll * sm_count(), 256, 3);
-  l.n_split = sh.n_split;
-  l.chunk = sh.chunk;
-  const size_t parts = sh.n_most > 1 ? (size_t)N * Hkv * R * sh.n_most : 0;
-  l.ml = 256;
+  l.n_split = 1;
+  l.chunk = 1;
+  l.stream = false;
+  size_t parts = 0;
+  int64_t blocks;
+  if (tc) {
+    const Shares sh = choose_split(units, max_len, sm_count(), 512);
+    l.n_split = sh.n_split;
+    l.chunk = sh.chunk;
+    blocks = units * l.n_split;
+    parts = sh.n_most > 1 ? (size_t)N * Hkv * R * sh.n_most : 0;
+  } else {
+    // Shares of equal work for what fills the SMs a few times at most.  A short
+    // history is done by one block for each unit without the join, and with many
+    // units the order in which blocks come evens them out.
+    const int64_t slots = (bf16 || l.rows_blk == 8 ? 2ll : 1ll) * sm_count();
+    l.stream = max_len > 512 && units < 16 * slots;
+    blocks = l.stream ? slots : units;
+    // (a workspace made for a longer history serves this one)
+    if (units < 16 * slots && max_len > 512) parts = (size_t)slots * 2 * l.rows_blk;
+  }
+  if (blocks > 0x7fffffffll) return false;
+  l.blocks = (int)blocks;
+  l.of = 256;
+  l.ml = align_up(l.of + (parts > 0 && !tc ? (size_t)units * sizeof(int2) : 0), 256);
   l.o = align_up(l.ml + parts * sizeof(float2), 256);
   l.total = align_up(l.o + parts * d * sizeof(float), 256);
-  return l;
+  return true;
 }
 
 template <int D>
@@ -692,13 +773,14 @@ cudaError_t run_all(const AttnArgs& a, bool bf16, int N, cudaStream_t s) {
     e = bf16 ? run<__nv_bfloat16, D, 1>(a, N, s) : run<float, D, 1>(a, N, s);
   else
     e = bf16 ? run<__nv_bfloat16, D, 2>(a, N, s) : run<float, D, 2>(a, N, s);
-  if (e != cudaSuccess || a.n_split == 1) return e;
+  if (e != cudaSuccess || (a.n_split == 1 && !a.stream)) return e;
   return bf16 ? join<__nv_bfloat16, D>(a, N, s) : join<float, D>(a, N, s);
 }
 }  // namespace
 
 size_t kv4_attention_ws_bytes(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d) {
-  return layout(bf16, N, Hq, Hkv, Lq, max_len, d).total;
+  Layout l;
+  return layout(bf16, N, Hq, Hkv, Lq, max_len, d, l) ? l.total : 0;
 }
 
 cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* ws,
@@ -714,6 +796,7 @@ cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* 
   a.k_scales = static_cast<const uint8_t*>(c.k_scales);
   a.v_codes = static_cast<const uint8_t*>(c.v_codes);
   a.v_scales = static_cast<const uint8_t*>(c.v_scales);
+  a.N = c.N;
   a.Hkv = c.H;
   a.G = p.Hq / c.H;
   a.R = a.G * p.Lq;
@@ -723,13 +806,17 @@ cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* 
   a.causal = p.causal;
   a.scale_log2 = ldexpf(p.scale * 1.4426950408889634f, c.k_exp);
   a.out_scale = ldexpf(1.0f, c.v_exp);
-  const Layout l = layout(p.bf16, c.N, p.Hq, c.H, p.Lq, p.max_len, c.d);
+  Layout l;
+  if (!layout(p.bf16, c.N, p.Hq, c.H, p.Lq, p.max_len, c.d, l)) return cudaErrorInvalidValue;
   a.rows_blk = l.rows_blk;
   a.n_rb = l.n_rb;
   a.n_split = l.n_split;
   a.chunk = l.chunk;
+  a.stream = l.stream;
+  a.blocks = l.blocks;
   char* w = static_cast<char*>(ws);
   a.err = reinterpret_cast<int*>(w);
+  a.part_of = reinterpret_cast<int2*>(w + l.of);
   a.part_ml = reinterpret_cast<float2*>(w + l.ml);
   a.part_o = reinterpret_cast<float*>(w + l.o);
   return c.d == 128 ? run_all<128>(a, p.bf16, c.N, s) : run_all<64>(a, p.bf16, c.N, s);

@@ -441,11 +441,9 @@ cudaError_t run(const AttnArgs& a, int N, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (int64_t)N * a.Hkv * a.n_rb * a.n_split;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)a.blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
