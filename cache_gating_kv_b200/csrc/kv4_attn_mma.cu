@@ -139,6 +139,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
 
   __shared__ StreamShare<kThreads> share;
   __shared__ Piece piece;
+  __shared__ struct {
+    uint4 q[NR][P][KS / 2][32];
+    float fac[NR * 8];
+    int lim[NR * 8];
+  } qs;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -197,17 +202,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
 
   // Queries are the B operand: in k16 step s thread (g, t) holds elements
   // t E + 4 s .. + 3 of row g, times a power of two that brings the row's largest
-  // to 2^13.  Logits come out with the rows on the columns, 2 t and 2 t + 1.
-  uint32_t qb[NR][P][KS][2];
-  float fac[NR][2];   // of a logit, to base 2
-  int lim[NR][2];     // keys that the row sees
-  int lim_min = k_end;
-#pragma unroll
-  for (int m = 0; m < NR; ++m) {
+  // to 2^13.  Logits come out with the rows on the columns, 2 t and 2 t + 1.  One warp
+  // to eight rows converts them for all; they are read from shared memory at every
+  // step, since the 16 registers that they would take cost more.
+  if (warp >= 1 && warp <= NR) {
+    const int m = warp - 1;
     const int r = r_base + m * 8 + g;
     const bool have = r < a.R;
     const int i = r / a.G, hq = piece.hk * a.G + r % a.G;
-    const int row_lim = have ? min(k_end, row_keys(a, len, i)) : k_end;
     float f[E];
     load_q<T, E>(reinterpret_cast<const T*>(a.q) + piece.n * a.qs.n + hq * a.qs.h + i * a.qs.l + t * E,
                  have, f);
@@ -219,26 +221,23 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     int ex = (int)(__float_as_uint(top) >> 23) - 127;
     ex = top == 0.0f ? 0 : max(-100, min(ex, 127));
     const float down = __uint_as_float((uint32_t)(127 + 13 - ex) << 23);
-    const float row_fac = fmaxf(ldexpf(a.scale_log2, ex - 13), 1.2e-38f);  // never 0 * -inf
+    if (t == 0) {
+      qs.fac[m * 8 + g] = fmaxf(ldexpf(a.scale_log2, ex - 13), 1.2e-38f);  // never 0 * -inf
+      qs.lim[m * 8 + g] = have ? min(k_end, row_keys(a, len, i)) : k_end;
+    }
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
+    for (int w = 0; w < KS / 2; ++w) {
+      uint32_t q[4], rest[4];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const float lo = f[4 * s + 2 * w] * down, hi = f[4 * s + 2 * w + 1] * down;
-        const uint32_t h = pack_f16(lo, hi);
-        qb[m][0][s][w] = h;
-        if constexpr (kF32) qb[m][P - 1][s][w] = rest_f16(h, lo, hi);
+      for (int x = 0; x < 4; ++x) {
+        const float lo = f[8 * w + 2 * x] * down, hi = f[8 * w + 2 * x + 1] * down;
+        q[x] = pack_f16(lo, hi);
+        if constexpr (kF32) rest[x] = rest_f16(q[x], lo, hi);
       }
+      qs.q[m][0][w][lane] = make_uint4(q[0], q[1], q[2], q[3]);
+      if constexpr (kF32) qs.q[m][P - 1][w][lane] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
     }
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      fac[m][c] = __shfl_sync(0xffffffffu, row_fac, (2 * t + c) * 4);
-      lim[m][c] = __shfl_sync(0xffffffffu, row_lim, (2 * t + c) * 4);
-    }
-    lim_min = min(lim_min, row_lim);
   }
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
 
   float acc[NR][MT][4];  // (element g or g + 8 of the m16 tile, row 2 t or 2 t + 1)
   float mref[NR][2], lsum[NR][2];
@@ -251,7 +250,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     mref[m][0] = mref[m][1] = -INFINITY;
     lsum[m][0] = lsum[m][1] = 0.0f;
   }
-  __syncthreads();  // the barriers are there
+  __syncthreads();  // the barriers and the queries are there
+  float fac[NR][2];  // of a logit, to base 2
+  int lim[NR][2];    // keys that the row sees
+  int lim_min = k_end;
+#pragma unroll
+  for (int m = 0; m < NR; ++m) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      fac[m][c] = qs.fac[m * 8 + 2 * t + c];
+      lim[m][c] = qs.lim[m * 8 + 2 * t + c];
+    }
+    lim_min = min(lim_min, qs.lim[m * 8 + g]);
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
 
   // Row g of the 8 keys j is key 8 j + kap: with this order neither the loads of
   // keys nor those of values (four rows at once) meet a bank twice.
@@ -285,6 +298,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     }
 #pragma unroll
     for (int w = 0; w < E / 8; ++w) {
+      uint4 qw[NR][P];
+#pragma unroll
+      for (int m = 0; m < NR; ++m)
+#pragma unroll
+        for (int q = 0; q < P; ++q) qw[m][q] = qs.q[m][q][w][lane];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         uint32_t p[2][4];
@@ -302,10 +320,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             if (w == 0 && q == 0)
-              mma_first(sc[m][u], a0, qb[m][q][0][0], qb[m][q][0][1]);
+              mma_first(sc[m][u], a0, qw[m][q].x, qw[m][q].y);
             else
-              mma_add(sc[m][u], a0, qb[m][q][2 * w][0], qb[m][q][2 * w][1]);
-            mma_add(sc[m][u], a1, qb[m][q][2 * w + 1][0], qb[m][q][2 * w + 1][1]);
+              mma_add(sc[m][u], a0, qw[m][q].x, qw[m][q].y);
+            mma_add(sc[m][u], a1, qw[m][q].z, qw[m][q].w);
           }
       }
     }

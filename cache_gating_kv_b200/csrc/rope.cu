@@ -16,6 +16,7 @@ namespace fc {
 namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // rows a thread loads before it stores the first
+constexpr int kLogTokens = 3;  // tokens of a block: at most 8
 
 struct RopeArgs {
   const uint8_t* x;
@@ -25,7 +26,7 @@ struct RopeArgs {
   int N, H, L, d;
   int T, log_t;        // tokens of a block, a power of two
   int HG, n_hg, n_lt;  // heads of a block, head groups, token tiles
-  int upr;             // units of a row
+  int upr, rpi;        // units of a row, rows of a pass
   bool inverse;
 };
 
@@ -60,7 +61,9 @@ __device__ __forceinline__ uint4 pack16(const float* f) {
 template <typename T, bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kThreads)
     rope_kernel(const RopeArgs a, const __grid_constant__ fc_rope_plan plan) {
-  extern __shared__ float2 cs[];  // [T][rot/2]
+  extern __shared__ float2 cs[];  // [T][rot/2], behind the turns and the axes
+  double* turns = reinterpret_cast<double*>(cs + a.T * (plan.rot_dim / 2));
+  uint8_t* axes = reinterpret_cast<uint8_t*>(turns + plan.rot_dim / 2);
   constexpr int V = 16 / (int)sizeof(T);
   const int half = plan.rot_dim / 2;
   int b = blockIdx.x;
@@ -69,15 +72,23 @@ __global__ void __launch_bounds__(kThreads)
   const int l0 = (b % a.n_lt) * a.T;
   const int n = b / a.n_lt;
   const int nt = min(a.T, a.L - l0);
+  // Lanes of a warp want different frequencies, which the constant bank would hand
+  // out one at a time.
+  for (int f = threadIdx.x; f < half; f += kThreads) {
+    turns[f] = plan.turns[f];
+    axes[f] = plan.axis[f];
+  }
+  __syncthreads();
   grid_dep_wait();
+  grid_dep_launch();
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int t = i / half, f = i - t * half;
-    const int32_t p = __ldg(a.pos + ((int64_t)plan.axis[f] * a.N + n) * a.L + l0 + t);
-    cs[i] = rope_cs(p, plan.turns[f], plan.m, a.inverse);
+    const int32_t p = __ldg(a.pos + ((int64_t)axes[f] * a.N + n) * a.L + l0 + t);
+    cs[i] = rope_cs(p, turns[f], plan.m, a.inverse);
   }
   __syncthreads();
   const int h0 = hg * a.HG, nh = min(a.HG, a.H - h0);
-  const int rpi = kThreads / a.upr;
+  const int rpi = a.rpi;  // a multiple of T: a thread keeps its token and its angles
   const int u = threadIdx.x % a.upr;
   const int r0 = threadIdx.x / a.upr;
   if (r0 >= rpi) return;
@@ -90,44 +101,50 @@ __global__ void __launch_bounds__(kThreads)
     const int pu = kHalf ? half / V : plan.rot_dim / V;  // units that rotate
     const bool rot = u < pu;
     const int e0 = rot ? u * V : plan.rot_dim + (u - pu) * V;
+    const int t = r0 & (a.T - 1);
+    if (t >= nt) return;
+    constexpr int kPairs = kHalf ? V : V / 2;
+    float2 c[kPairs];
+    if (rot) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) c[i] = cs[t * half + u * kPairs + i];
+    }
+    x += (int64_t)(l0 + t) * a.xs.l + e0;
+    y += (int64_t)(l0 + t) * a.ys.l + e0;
     for (int r = r0; r < rows; r += rpi * kUnroll) {
       uint4 va[kUnroll], vb[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        const int q = r + k * rpi, t = q & (a.T - 1);
-        if (q < rows && t < nt) {
-          const T* p = x + (int64_t)(q >> a.log_t) * a.xs.h + (int64_t)(l0 + t) * a.xs.l + e0;
+        const int q = r + k * rpi;
+        if (q < rows) {
+          const T* p = x + (int64_t)(q >> a.log_t) * a.xs.h;
           va[k] = *reinterpret_cast<const uint4*>(p);
           if (kHalf && rot) vb[k] = *reinterpret_cast<const uint4*>(p + half);
         }
       }
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        const int q = r + k * rpi, t = q & (a.T - 1);
-        if (q >= rows || t >= nt) continue;
-        T* p = y + (int64_t)(q >> a.log_t) * a.ys.h + (int64_t)(l0 + t) * a.ys.l + e0;
+        const int q = r + k * rpi;
+        if (q >= rows) continue;
+        T* p = y + (int64_t)(q >> a.log_t) * a.ys.h;
         if (rot) {
           float f[V], g[V];
           Vec16<T>::to_float(va[k], f);
           if constexpr (kHalf) {
-            const float2* c = cs + t * half + u * V;
             Vec16<T>::to_float(vb[k], g);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-              const float2 w = c[i];
               const float f0 = f[i];
-              f[i] = rope_a(f0, g[i], w);
-              g[i] = rope_b(f0, g[i], w);
+              f[i] = rope_a(f0, g[i], c[i]);
+              g[i] = rope_b(f0, g[i], c[i]);
             }
             *reinterpret_cast<uint4*>(p + half) = pack16<T>(g);
           } else {
-            const float2* c = cs + t * half + u * (V / 2);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
-              const float2 w = c[i];
               const float f0 = f[2 * i];
-              f[2 * i] = rope_a(f0, f[2 * i + 1], w);
-              f[2 * i + 1] = rope_b(f0, f[2 * i + 1], w);
+              f[2 * i] = rope_a(f0, f[2 * i + 1], c[i]);
+              f[2 * i + 1] = rope_b(f0, f[2 * i + 1], c[i]);
             }
           }
           *reinterpret_cast<uint4*>(p) = pack16<T>(f);
@@ -163,16 +180,17 @@ cudaError_t run(RopeArgs a, const fc_rope_plan& plan, cudaStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
   const int half = plan.rot_dim / 2;
   a.upr = !kVec ? a.d / 2 : kHalf ? half / V + (a.d - plan.rot_dim) / V : a.d / V;
-  const int rpi = kThreads / a.upr;
+  a.rpi = kThreads / a.upr;
   a.log_t = 0;
-  while (a.log_t < 4 && (1 << a.log_t) < a.L) ++a.log_t;
+  while (a.log_t < kLogTokens && (1 << a.log_t) < a.L && (2 << a.log_t) <= a.rpi) ++a.log_t;
   a.T = 1 << a.log_t;
+  a.rpi &= ~(a.T - 1);
   a.n_lt = (int)ceil_div(a.L, a.T);
-  // Fewer heads to a block (each block computes its angles anew) only while
-  // the grid would leave SMs without work and a block keeps a full pass.
+  // Fewer heads to a block (each block computes its angles anew) only while the grid
+  // would leave SMs without work and a block keeps a full pass.
   a.HG = a.H;
-  const int64_t want = 6ll * sm_count(), tiles = (int64_t)a.N * a.n_lt;
-  while (a.HG > 1 && tiles * ceil_div(a.H, a.HG) < want && (a.HG + 1) / 2 * a.T >= rpi)
+  const int64_t want = 4ll * sm_count(), tiles = (int64_t)a.N * a.n_lt;
+  while (a.HG > 1 && tiles * ceil_div(a.H, a.HG) < want && (a.HG + 1) / 2 * a.T >= a.rpi)
     a.HG = (a.HG + 1) / 2;
   a.n_hg = (int)ceil_div(a.H, a.HG);
   const int64_t blocks = tiles * a.n_hg;
@@ -181,7 +199,7 @@ cudaError_t run(RopeArgs a, const fc_rope_plan& plan, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)a.T * half * sizeof(float2);
+  cfg.dynamicSmemBytes = (size_t)half * (a.T * sizeof(float2) + sizeof(double) + 1);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
