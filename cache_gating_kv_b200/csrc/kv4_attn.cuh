@@ -21,6 +21,7 @@ struct AttnArgs {
   int n_split, chunk;
   bool stream;                         // shares of equal work (StreamShare)
   int blocks;                          // of the grid that computes
+  bool joined;                         // a second kernel follows
   bool causal;
   float scale_log2;  // scale * 2^k_exp * log2 e
   float out_scale;   // 2^v_exp
@@ -32,7 +33,7 @@ struct AttnArgs {
 
 __device__ __forceinline__ int seq_len(const AttnArgs& a, int n) {
   if (a.lens == nullptr) return a.max_len;
-  return max(0, min(__ldg(a.lens + n), a.max_len));
+  return max(0, min(a.lens[n], a.max_len));
 }
 // Keys that query i sees.
 __device__ __forceinline__ int row_keys(const AttnArgs& a, int len, int i) {

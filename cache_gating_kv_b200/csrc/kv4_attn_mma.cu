@@ -107,7 +107,7 @@ __device__ __forceinline__ void load_q(const T* p, bool have, float (&f)[E]) {
 #pragma unroll
   for (int i = 0; i < E / V; ++i) {
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (have) w = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    if (have) w = reinterpret_cast<const uint4*>(p)[i];
     Vec16<T>::to_float(w, f + i * V);
   }
 }
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     tc::fence_barrier_init();
   }
   grid_dep_wait();
-  grid_dep_launch();
+  if (a.joined) grid_dep_launch();
 
   // The block's share: one unit, or a run of stages over units.
   if (a.stream) share.begin(a, kLeastStages);
@@ -617,7 +617,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
   const float4* po = reinterpret_cast<const float4*>(a.part_o + row * a.n_split * D) + lane;
   int step = 1;  // rows between parts
   grid_dep_wait();
-  grid_dep_launch();
   if (a.stream) {
     ns = 0;
     if (k_top > 0) {
@@ -791,7 +790,7 @@ cudaError_t run_all(const AttnArgs& a, bool bf16, int N, cudaStream_t s) {
     e = bf16 ? run<__nv_bfloat16, D, 1>(a, N, s) : run<float, D, 1>(a, N, s);
   else
     e = bf16 ? run<__nv_bfloat16, D, 2>(a, N, s) : run<float, D, 2>(a, N, s);
-  if (e != cudaSuccess || (a.n_split == 1 && !a.stream)) return e;
+  if (e != cudaSuccess || !a.joined) return e;
   return bf16 ? join<__nv_bfloat16, D>(a, N, s) : join<float, D>(a, N, s);
 }
 }  // namespace
@@ -831,6 +830,7 @@ cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* 
   a.n_split = l.n_split;
   a.chunk = l.chunk;
   a.stream = l.stream;
+  a.joined = l.stream || l.n_split > 1;
   a.blocks = l.blocks;
   char* w = static_cast<char*>(ws);
   a.err = reinterpret_cast<int*>(w);

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_slot;
   grid_dep_wait();
-  grid_dep_launch();
+  if (a.joined) grid_dep_launch();
 
   const int len = seq_len(a, n);
   const int r_base = rb * kTcRows;
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       uint32_t top2 = 0;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
-        w[c] = have ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        w[c] = have ? src[c] : make_uint4(0u, 0u, 0u, 0u);
         top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu),
                                        __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu)));
       }

@@ -16,6 +16,7 @@ namespace fc {
 
 namespace {
 constexpr int kThreads = 256;
+constexpr int kLoadRows = 4;  // rows of a thread that reads the cache
 
 // 16 consecutive elements as float32.
 template <typename T>
@@ -23,47 +24,65 @@ __device__ __forceinline__ void load16(const T* p, float (&f)[16]) {
   constexpr int V = 16 / (int)sizeof(T);
 #pragma unroll
   for (int i = 0; i < 16 / V; ++i)
-    Vec16<T>::to_float(__ldg(reinterpret_cast<const uint4*>(p) + i), f + i * V);
+    Vec16<T>::to_float(reinterpret_cast<const uint4*>(p)[i], f + i * V);
 }
 
 template <typename T>
 __device__ __forceinline__ float load1(const T* p) {
   if constexpr (sizeof(T) == 4)
-    return __ldg(p);
+    return *p;
   else
-    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
+    return __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16);
 }
 
-// One group of 16 numbers to its scale byte and its eight code bytes.
-__device__ __forceinline__ uint2 quantise16(float (&y)[16], uint32_t& scale) {
-  uint32_t top = 0;  // bits of max |y|: NaN counts above infinity
+// The largest |x| of 16 raw elements; NaN if one of them is.
+__device__ __forceinline__ float absmax16(const uint4 (&w)[2], __nv_bfloat16) {
+  __nv_bfloat162 m = __habs2(reinterpret_cast<const __nv_bfloat162&>(w[0].x));
+  const uint32_t u[7] = {w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
-  const float amax = __uint_as_float(top);
-  if (top > 0x7f800000u) {  // a NaN: the group reads as NaN
-    scale = 0x7Fu;
-    return make_uint2(0u, 0u);
-  }
-  // Numbers beyond 6 * 448 saturate whatever they are; cutting them there
-  // keeps the quotients below finite (their scale is 448).
-  if (amax > 4096.0f) {
+  for (int i = 0; i < 7; ++i)
+    m = __hmax2_nan(m, __habs2(reinterpret_cast<const __nv_bfloat162&>(u[i])));
+  return __bfloat162float(__hmax_nan(m.x, m.y));
+}
+__device__ __forceinline__ float absmax16(const float (&x)[16]) {
+  uint32_t top = 0;  // as bits: NaN counts above infinity
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = fminf(fmaxf(y[i], -4096.0f), 4096.0f);
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  return __uint_as_float(top);
+}
+
+// One group of 16 numbers x with their largest to its scale byte and its eight code
+// bytes; `down` and `up` are 2^-exp and 2^exp, powers of two that are multiplied into
+// the scale and its reciprocal instead of every element.
+__device__ __forceinline__ uint2 quantise16(float (&x)[16], float amax, float down, float up,
+                                            uint32_t& scale) {
+  amax *= down;
+  if (!(amax <= 4096.0f)) {
+    if (amax != amax) {  // the group reads as NaN
+      scale = 0x7Fu;
+      return make_uint2(0u, 0u);
+    }
+    // Numbers beyond 6 * 448 saturate whatever they are; cutting them here keeps
+    // the quotients below finite (their scale is 448).
+    const float cut = 4096.0f * up;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -cut), cut);
   }
   scale = kv4::f32_to_e4m3(fminf(__fdiv_rn(amax, 6.0f), 448.0f));
-  const float s = kv4::lo_f16(kv4::e4m3x2_to_f16x2(scale));
+  float s = kv4::lo_f16(kv4::e4m3x2_to_f16x2(scale));
   // y / s rounded to nearest, so that a number half way between two codes is
   // seen as such: from the correctly rounded reciprocal r, q = y r is within an
   // ulp and q - r (q s - y) is the rounded quotient (Markstein, "Computation of
   // elementary functions on the IBM RISC System/6000 processor", 1990); with the
   // remainder in this order a zero keeps its sign.
-  const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+  const float r = s > 0.0f ? __frcp_rn(s) * down : 0.0f;
+  s *= up;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float q = __fmul_rn(y[i], r);
-    y[i] = __fmaf_rn(-__fmaf_rn(q, s, -y[i]), r, q);
+    const float q = __fmul_rn(x[i], r);
+    x[i] = __fmaf_rn(-__fmaf_rn(q, s, -x[i]), r, q);
   }
-  return make_uint2(kv4::f32x8_to_e2m1(y), kv4::f32x8_to_e2m1(y + 8));
+  return make_uint2(kv4::f32x8_to_e2m1(x), kv4::f32x8_to_e2m1(x + 8));
 }
 
 struct StoreArgs {
@@ -71,7 +90,7 @@ struct StoreArgs {
   Strides st[2];
   uint8_t* codes[2];
   uint8_t* scales[2];
-  float down[2];  // 2^-exp
+  float down[2], up[2];  // 2^-exp, 2^exp
   const int32_t* idx;
   const int32_t* row0_dev;
   const int32_t* pos;
@@ -82,7 +101,7 @@ struct StoreArgs {
 // Source row of result row r (-1: zeros).
 __device__ __forceinline__ int source_row(const StoreArgs& a, int64_t nh, int r) {
   if (a.idx == nullptr) return r;
-  const int j = __ldg(a.idx + nh * a.rows + r);
+  const int j = a.idx[nh * a.rows + r];
   return j >= 0 && j < a.L ? j : -1;
 }
 
@@ -90,9 +109,11 @@ __device__ __forceinline__ int source_row(const StoreArgs& a, int64_t nh, int r)
 template <typename T, int D, int kRope>
 __global__ void __launch_bounds__(kThreads)
     store_kernel(const StoreArgs a, const __grid_constant__ fc_rope_plan plan) {
-  extern __shared__ float2 cs[];
-  constexpr int G = D / 16;  // groups (and threads) of a row
+  extern __shared__ float2 cs[];  // [T][rot/2], behind the turns and the axes
+  constexpr int G = D / 16;       // groups (and threads) of a row
   constexpr int kRowsPerPass = kThreads / G;
+  constexpr int kRaw = (int)sizeof(T);  // 16-byte vectors of a group: 2 (bf16), 4
+  constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;  // rows loaded before the first is stored
   const int kv = blockIdx.y;  // 0 keys, 1 values
   int b = blockIdx.x;
   const int hg = b % a.n_hg;
@@ -100,40 +121,72 @@ __global__ void __launch_bounds__(kThreads)
   const int l0 = (b % a.n_lt) * a.T;
   const int n = b / a.n_lt;
   const int nt = min(a.T, a.rows - l0);
-  grid_dep_wait();
   const bool rotate = kRope != 0 && kv == 0;
   const int half = plan.rot_dim / 2;
-  if (rotate) {
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-      const int t = i / half, f = i - t * half;
-      const int32_t p = __ldg(a.pos + ((int64_t)plan.axis[f] * a.N + n) * a.L + l0 + t);
-      cs[i] = rope_cs(p, plan.turns[f], plan.m, false);
+  double* turns = reinterpret_cast<double*>(cs + a.T * half);
+  uint8_t* axes = reinterpret_cast<uint8_t*>(turns + half);
+  if (rotate) {  // (lanes want different frequencies: see the rotation's kernel)
+    for (int f = threadIdx.x; f < half; f += kThreads) {
+      turns[f] = plan.turns[f];
+      axes[f] = plan.axis[f];
     }
     __syncthreads();
   }
-  const int first = a.row0_dev != nullptr ? __ldg(a.row0_dev + n) : a.row0;
+  grid_dep_wait();
+  if (rotate) {
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+      const int t = i / half, f = i - t * half;
+      const int32_t p = a.pos[((int64_t)axes[f] * a.N + n) * a.L + l0 + t];
+      cs[i] = rope_cs(p, turns[f], plan.m, false);
+    }
+    __syncthreads();
+  }
+  const int first = a.row0_dev != nullptr ? a.row0_dev[n] : a.row0;
   const int h0 = hg * a.HG, nh = min(a.HG, a.H - h0);
   const int g = threadIdx.x % G;
   const Strides st = a.st[kv];
-  const T* src = reinterpret_cast<const T*>(a.src[kv]) + n * st.n;
+  const T* src = reinterpret_cast<const T*>(a.src[kv]) + n * st.n + g * 16;
+  const float down = a.down[kv], up = a.up[kv];
   const int rows = nh << a.log_t;
-  for (int r = threadIdx.x / G; r < rows; r += kRowsPerPass) {
-    const int t = r & (a.T - 1), h = h0 + (r >> a.log_t);
-    const int64_t dst = (int64_t)first + l0 + t;
-    if (t >= nt || dst < 0 || dst >= a.cap) continue;
-    const int64_t nhi = (int64_t)n * a.H + h;
-    const int j = source_row(a, nhi, l0 + t);
-    float y[16];
-    if (j >= 0) {
-      const T* row = src + h * st.h + (int64_t)j * st.l;
-      load16(row + g * 16, y);
-      if (rotate && g * 16 < plan.rot_dim) {
-        const float2* c = cs + t * half;
+  for (int r0 = threadIdx.x / G; r0 < rows; r0 += kRowsPerPass * kUnroll) {
+    int64_t dst[kUnroll];  // row of the cache, -1: none
+    const T* from[kUnroll];
+    int j[kUnroll];        // source row, -1: zeros
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int r = r0 + k * kRowsPerPass;
+      const int t = r & (a.T - 1), h = h0 + (r >> a.log_t);
+      const int64_t at = (int64_t)first + l0 + t;
+      dst[k] = -1;
+      if (r >= rows || t >= nt || at < 0 || at >= a.cap) continue;
+      const int64_t nhi = (int64_t)n * a.H + h;
+      dst[k] = nhi * a.cap + at;
+      j[k] = source_row(a, nhi, l0 + t);
+      from[k] = src + h * st.h + (int64_t)max(j[k], 0) * st.l;
+    }
+    uint4 raw[kUnroll][kRaw];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+#pragma unroll
+      for (int i = 0; i < kRaw; ++i) {
+        raw[k][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (dst[k] >= 0 && j[k] >= 0) raw[k][i] = reinterpret_cast<const uint4*>(from[k])[i];
+      }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      if (dst[k] < 0) continue;
+      float y[16];
+#pragma unroll
+      for (int i = 0; i < kRaw; ++i) Vec16<T>::to_float(raw[k][i], y + i * (16 / kRaw));
+      const bool turn = rotate && g * 16 < plan.rot_dim;
+      if (turn) {
+        const float2* c = cs + ((r0 + k * kRowsPerPass) & (a.T - 1)) * half;
         if constexpr (kRope == 1) {
+          const T* row = from[k] - g * 16;
           if (half % 16 == 0) {  // the group and its partners are whole groups
             float z[16];
             const bool low = g * 16 < half;
-            load16(row + g * 16 + (low ? half : -half), z);
+            load16(from[k] + (low ? half : -half), z);
             c += low ? g * 16 : g * 16 - half;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -148,7 +201,7 @@ __global__ void __launch_bounds__(kThreads)
                 y[i] = rope_b(load1(row + e - half), y[i], c[e - half]);
             }
           }
-        } else {
+        } else if constexpr (kRope == 2) {
           c += g * 8;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -160,34 +213,38 @@ __global__ void __launch_bounds__(kThreads)
           }
         }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = 0.0f;
+      float amax;
+      if constexpr (sizeof(T) == 2)
+        amax = turn ? absmax16(y) : absmax16(raw[k], T());
+      else
+        amax = absmax16(y);
+      uint32_t scale;
+      const uint2 codes = quantise16(y, amax, down, up, scale);
+      const int64_t at = dst[k] * G + g;
+      reinterpret_cast<uint2*>(a.codes[kv])[at] = codes;
+      a.scales[kv][at] = (uint8_t)scale;
     }
-    const float down = a.down[kv];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], down);
-    uint32_t scale;
-    const uint2 codes = quantise16(y, scale);
-    const int64_t at = (nhi * a.cap + dst) * G + g;
-    reinterpret_cast<uint2*>(a.codes[kv])[at] = codes;
-    a.scales[kv][at] = (uint8_t)scale;
   }
 }
 
 template <typename T, int D>
 cudaError_t run_store(StoreArgs a, const fc_rope_plan* plan, cudaStream_t s) {
   constexpr int kRowsPerPass = kThreads / (D / 16);
+  constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
+  // Rotated keys: few tokens and many heads to a block, which share the angles.
+  // Otherwise a run of tokens, whose rows (or kept rows) lie close together.
+  const int most = plan != nullptr ? 3 : 7;
   a.log_t = 0;
-  while (a.log_t < 4 && (1 << a.log_t) < a.rows) ++a.log_t;
+  while (a.log_t < most && (1 << a.log_t) < a.rows) ++a.log_t;
   a.T = 1 << a.log_t;
   a.n_lt = (int)ceil_div(a.rows, a.T);
   a.HG = a.H;
-  // as for the rotation alone: split the heads while SMs would be idle, and
-  // without angles to share down to one pass of a block
-  const int64_t want = plan != nullptr ? 6ll * sm_count() : INT64_MAX;
+  // the heads split while SMs would be idle, and without angles to share down to
+  // what a block's threads load at once
+  const int64_t want = plan != nullptr ? 3ll * sm_count() : INT64_MAX;
   const int64_t tiles = (int64_t)a.N * a.n_lt;
-  while (a.HG > 1 && tiles * ceil_div(a.H, a.HG) < want && (a.HG + 1) / 2 * a.T >= kRowsPerPass)
+  const int least = plan != nullptr ? kRowsPerPass : kRowsPerPass * kUnroll;
+  while (a.HG > 1 && tiles * ceil_div(a.H, a.HG) < want && (a.HG + 1) / 2 * a.T >= least)
     a.HG = (a.HG + 1) / 2;
   a.n_hg = (int)ceil_div(a.H, a.HG);
   const int64_t blocks = tiles * a.n_hg;
@@ -204,7 +261,8 @@ cudaError_t run_store(StoreArgs a, const fc_rope_plan* plan, cudaStream_t s) {
   if (plan == nullptr) {
     e = cudaLaunchKernelEx(&cfg, store_kernel<T, D, 0>, a, none);
   } else {
-    cfg.dynamicSmemBytes = (size_t)a.T * (plan->rot_dim / 2) * sizeof(float2);
+    cfg.dynamicSmemBytes =
+        (size_t)(plan->rot_dim / 2) * (a.T * sizeof(float2) + sizeof(double) + 1);
     e = plan->layout == FC_ROPE_HALF ? cudaLaunchKernelEx(&cfg, store_kernel<T, D, 1>, a, *plan)
                                      : cudaLaunchKernelEx(&cfg, store_kernel<T, D, 2>, a, *plan);
   }
@@ -224,61 +282,69 @@ struct LoadArgs {
   int n_lt;  // row tiles of a head
 };
 
+// A thread takes 8 codes, for bf16 16 bytes of numbers, so that a warp's stores are
+// whole lines (with 16 numbers to a thread every store covered half sectors: 4.7 of
+// 6.6 TB/s).
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) load_kernel(const LoadArgs a) {
-  constexpr int G = D / 16;
-  constexpr int V = 16 / (int)sizeof(T);
-  constexpr int kRowsPerPass = kThreads / G;
+  constexpr int TPR = D / 8;  // threads of a row
+  constexpr int kRowsPerPass = kThreads / TPR;
   grid_dep_wait();
   const int kv = blockIdx.y;
   const int nh = blockIdx.x / a.n_lt;
-  const int l = (blockIdx.x % a.n_lt) * kRowsPerPass + threadIdx.x / G;
-  const int g = threadIdx.x % G;
-  if (l >= a.L) return;
+  const int l0 = (blockIdx.x % a.n_lt) * (kRowsPerPass * kLoadRows) + threadIdx.x / TPR;
+  const int c = threadIdx.x % TPR;
   const int n = nh / a.H, h = nh % a.H;
-  const int64_t src = (int64_t)(a.row0_dev != nullptr ? __ldg(a.row0_dev + n) : a.row0) + l;
-  float f[16];
-  if (src >= 0 && src < a.cap) {
-    const int64_t at = ((int64_t)nh * a.cap + src) * G + g;
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(a.codes[kv]) + at);
-    const uint32_t sb = __ldg(a.scales[kv] + at);
-    const float s = __fmul_rn(kv4::lo_f16(kv4::e4m3x2_to_f16x2(sb)), a.up[kv]);
-    uint32_t p[8];
-    kv4::e2m1x8_to_f16x2(c.x, reinterpret_cast<uint32_t(&)[4]>(p[0]));
-    kv4::e2m1x8_to_f16x2(c.y, reinterpret_cast<uint32_t(&)[4]>(p[4]));
+  const int64_t first = a.row0_dev != nullptr ? a.row0_dev[n] : a.row0;
+  const Strides st = a.st[kv];
+  T* out = reinterpret_cast<T*>(a.dst[kv]) + n * st.n + h * st.h + c * 8;
+  const float up = a.up[kv];
+  uint32_t code[kLoadRows], sb[kLoadRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+  for (int k = 0; k < kLoadRows; ++k) {
+    const int l = l0 + k * kRowsPerPass;
+    const int64_t src = first + l;
+    code[k] = sb[k] = 0;
+    if (l < a.L && src >= 0 && src < a.cap) {
+      const int64_t row = (int64_t)nh * a.cap + src;
+      code[k] = reinterpret_cast<const uint32_t*>(a.codes[kv] + row * (D / 2))[c];
+      sb[k] = a.scales[kv][row * (D / 16) + (c >> 1)];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kLoadRows; ++k) {
+    const int l = l0 + k * kRowsPerPass;
+    if (l >= a.L) return;
+    const float s = kv4::lo_f16(kv4::e4m3x2_to_f16x2(sb[k])) * up;
+    uint32_t p[4];
+    kv4::e2m1x8_to_f16x2(code[k], p);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       f[2 * i] = kv4::lo_f16(p[i]) * s;
       f[2 * i + 1] = kv4::lo_f16(p[i] >> 16) * s;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = 0.0f;
-  }
-  const Strides st = a.st[kv];
-  T* out = reinterpret_cast<T*>(a.dst[kv]) + n * st.n + h * st.h + (int64_t)l * st.l + g * 16;
-#pragma unroll
-  for (int i = 0; i < 16 / V; ++i) {
-    uint4 w;
+    uint4* w = reinterpret_cast<uint4*>(out + (int64_t)l * st.l);
     if constexpr (sizeof(T) == 4) {
-      w = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
-                     __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+      w[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                        __float_as_uint(f[3]));
+      w[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                        __float_as_uint(f[7]));
     } else {  // exact: the products have at most 6 significant bits
       uint32_t u[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[8 * i + 2 * j], f[8 * i + 2 * j + 1]);
-        u[j] = reinterpret_cast<const uint32_t&>(b);
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        u[i] = reinterpret_cast<const uint32_t&>(b);
       }
-      w = make_uint4(u[0], u[1], u[2], u[3]);
+      *w = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    reinterpret_cast<uint4*>(out)[i] = w;
   }
 }
 
 template <typename T, int D>
 cudaError_t run_load(LoadArgs a, int N, cudaStream_t s) {
-  a.n_lt = (int)ceil_div(a.L, kThreads / (D / 16));
+  a.n_lt = (int)ceil_div(a.L, kThreads * 8 / D * kLoadRows);
   const int64_t blocks = (int64_t)N * a.H * a.n_lt;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
@@ -310,6 +376,8 @@ cudaError_t launch_kv4_store(const void* k, const void* v, bool bf16, int L, Str
   a.scales[1] = static_cast<uint8_t*>(c.v_scales);
   a.down[0] = ldexpf(1.0f, -c.k_exp);
   a.down[1] = ldexpf(1.0f, -c.v_exp);
+  a.up[0] = ldexpf(1.0f, c.k_exp);
+  a.up[1] = ldexpf(1.0f, c.v_exp);
   a.idx = idx;
   a.row0_dev = row0_dev;
   a.pos = pos;

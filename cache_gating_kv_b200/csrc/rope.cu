@@ -80,10 +80,9 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   grid_dep_wait();
-  grid_dep_launch();
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int t = i / half, f = i - t * half;
-    const int32_t p = __ldg(a.pos + ((int64_t)axes[f] * a.N + n) * a.L + l0 + t);
+    const int32_t p = a.pos[((int64_t)axes[f] * a.N + n) * a.L + l0 + t];
     cs[i] = rope_cs(p, turns[f], plan.m, a.inverse);
   }
   __syncthreads();
