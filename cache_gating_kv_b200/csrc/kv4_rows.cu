@@ -8,9 +8,12 @@
 // the way the thread also reads the partner elements of its group (the same
 // lines, read by another thread of the warp, so they come from L1) instead of
 // exchanging numbers through shared memory.
+#include <cuda.h>
+
 #include "fc_common.cuh"
 #include "fc_kernels.h"
 #include "kv4.cuh"
+#include "tc_ptx.cuh"
 
 namespace fc {
 
@@ -51,8 +54,8 @@ __device__ __forceinline__ float absmax16(const float (&x)[16]) {
   return __uint_as_float(top);
 }
 
-// One group of 16 numbers x with their largest to its scale byte and its eight code
-// bytes; `down` and `up` are 2^-exp and 2^exp, powers of two that are multiplied into
+// One group of 16 numbers, given as their negatives x with the largest |x|, to its
+// scale byte and its eight code bytes; `down` and `up` are 2^-exp and 2^exp, powers of two that are multiplied into
 // the scale and its reciprocal instead of every element.
 __device__ __forceinline__ uint2 quantise16(float (&x)[16], float amax, float down, float up,
                                             uint32_t& scale) {
@@ -68,19 +71,26 @@ __device__ __forceinline__ uint2 quantise16(float (&x)[16], float amax, float do
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -cut), cut);
   }
-  scale = kv4::f32_to_e4m3(fminf(__fdiv_rn(amax, 6.0f), 448.0f));
+  // (rounded quotients as below, the reciprocal of 6 being a constant)
+  constexpr float kSixth = 1.0f / 6.0f;
+  const float a6 = __fmul_rn(amax, kSixth);
+  scale = kv4::f32_to_e4m3(fminf(__fmaf_rn(-__fmaf_rn(a6, 6.0f, -amax), kSixth, a6), 448.0f));
   float s = kv4::lo_f16(kv4::e4m3x2_to_f16x2(scale));
   // y / s rounded to nearest, so that a number half way between two codes is
   // seen as such: from the correctly rounded reciprocal r, q = y r is within an
   // ulp and q - r (q s - y) is the rounded quotient (Markstein, "Computation of
-  // elementary functions on the IBM RISC System/6000 processor", 1990); with the
-  // remainder in this order a zero keeps its sign.
-  const float r = s > 0.0f ? __frcp_rn(s) * down : 0.0f;
+  // elementary functions on the IBM RISC System/6000 processor", 1990).  Two
+  // numbers to an instruction, from -y and -r; in this order a zero keeps its sign.
+  const float nr = s > 0.0f ? __frcp_rn(s) * -down : -0.0f;
   s *= up;
+  const float2 rr = make_float2(nr, nr), ss = make_float2(s, s);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float q = __fmul_rn(x[i], r);
-    x[i] = __fmaf_rn(-__fmaf_rn(q, s, -x[i]), r, q);
+  for (int i = 0; i < 16; i += 2) {
+    const float2 y = make_float2(x[i], x[i + 1]);  // negative
+    const float2 q = tc::fmul2(y, rr);
+    const float2 t = tc::ffma2(tc::ffma2(q, ss, y), rr, q);
+    x[i] = t.x;
+    x[i + 1] = t.y;
   }
   return make_uint2(kv4::f32x8_to_e2m1(x), kv4::f32x8_to_e2m1(x + 8));
 }
@@ -98,22 +108,15 @@ struct StoreArgs {
   int T, log_t, HG, n_hg, n_lt;
 };
 
-// Source row of result row r (-1: zeros).
-__device__ __forceinline__ int source_row(const StoreArgs& a, int64_t nh, int r) {
-  if (a.idx == nullptr) return r;
-  const int j = a.idx[nh * a.rows + r];
-  return j >= 0 && j < a.L ? j : -1;
-}
-
 // kRope: 0 none, 1 half layout, 2 interleaved.
 template <typename T, int D, int kRope>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kRope == 0 ? 4 : 2)
     store_kernel(const StoreArgs a, const __grid_constant__ fc_rope_plan plan) {
   extern __shared__ float2 cs[];  // [T][rot/2], behind the turns and the axes
   constexpr int G = D / 16;       // groups (and threads) of a row
   constexpr int kRowsPerPass = kThreads / G;
   constexpr int kRaw = (int)sizeof(T);  // 16-byte vectors of a group: 2 (bf16), 4
-  constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;  // rows loaded before the first is stored
+  constexpr int kUnroll = 2;  // rows loaded before the first is stored
   const int kv = blockIdx.y;  // 0 keys, 1 values
   int b = blockIdx.x;
   const int hg = b % a.n_hg;
@@ -141,28 +144,57 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
   }
-  const int first = a.row0_dev != nullptr ? a.row0_dev[n] : a.row0;
   const int h0 = hg * a.HG, nh = min(a.HG, a.H - h0);
   const int g = threadIdx.x % G;
   const Strides st = a.st[kv];
-  const T* src = reinterpret_cast<const T*>(a.src[kv]) + n * st.n + g * 16;
   const float down = a.down[kv], up = a.up[kv];
-  const int rows = nh << a.log_t;
-  for (int r0 = threadIdx.x / G; r0 < rows; r0 += kRowsPerPass * kUnroll) {
-    int64_t dst[kUnroll];  // row of the cache, -1: none
-    const T* from[kUnroll];
-    int j[kUnroll];        // source row, -1: zeros
+  // Pass by pass a thread goes on either by tokens of one head (T over the rows of a
+  // pass) or by heads of one token.
+  const bool by_token = a.T > kRowsPerPass;
+  const int step_t = by_token ? kRowsPerPass : 0;
+  const int step_h = by_token ? 0 : kRowsPerPass >> a.log_t;
+  int t = threadIdx.x / G & (a.T - 1), h = threadIdx.x / G >> a.log_t;
+  const int64_t nhi = (int64_t)n * a.H + h0 + h;
+  // tokens whose row lies in the cache
+  const int64_t row0 = (int64_t)(a.row0_dev != nullptr ? a.row0_dev[n] : a.row0) + l0;
+  const int t_min = (int)max((int64_t)0, min((int64_t)nt, -row0));
+  const int t_max = (int)max((int64_t)0, min((int64_t)nt, a.cap - row0));
+  // group of the cache, element of the source: of this pass, and on to the next
+  int64_t o = (nhi * a.cap + row0 + t) * G + g;
+  const int64_t o_step = ((int64_t)step_h * a.cap + step_t) * G;
+  const T* src = reinterpret_cast<const T*>(a.src[kv]) + n * st.n + (h0 + h) * st.h + g * 16;
+  const int32_t* idx = a.idx != nullptr ? a.idx + nhi * a.rows + l0 + t : nullptr;
+  const int64_t idx_step = (int64_t)step_h * a.rows + step_t;
+  const int64_t src_step = step_h * st.h + (idx == nullptr ? step_t * st.l : 0);
+  if (idx == nullptr) src += (int64_t)(l0 + t) * st.l;
+  uint2* const codes_out = reinterpret_cast<uint2*>(a.codes[kv]);
+  uint8_t* const scales_out = a.scales[kv];
+  const int64_t src_l = st.l;
+  const int L = a.L;
+  // The next pass's indices are loaded a pass ahead: they are the only load that
+  // another one waits for.
+  int ahead[kUnroll];
+#pragma unroll
+  for (int k = 0; k < kUnroll; ++k)
+    ahead[k] = idx != nullptr && t + k * step_t < nt && h + k * step_h < nh ? idx[k * idx_step] : 0;
+  while (t < t_max && h < nh) {
+    bool put[kUnroll];
+    const T* from[kUnroll]; // nullptr: zeros
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int r = r0 + k * kRowsPerPass;
-      const int t = r & (a.T - 1), h = h0 + (r >> a.log_t);
-      const int64_t at = (int64_t)first + l0 + t;
-      dst[k] = -1;
-      if (r >= rows || t >= nt || at < 0 || at >= a.cap) continue;
-      const int64_t nhi = (int64_t)n * a.H + h;
-      dst[k] = nhi * a.cap + at;
-      j[k] = source_row(a, nhi, l0 + t);
-      from[k] = src + h * st.h + (int64_t)max(j[k], 0) * st.l;
+      put[k] = t >= t_min && t < t_max && h < nh;
+      from[k] = src;
+      if (idx != nullptr)
+        from[k] = (unsigned)ahead[k] < (unsigned)L ? src + ahead[k] * src_l : nullptr;
+      t += step_t;
+      h += step_h;
+      src += src_step;
+    }
+    if (idx != nullptr) {
+      idx += kUnroll * idx_step;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        ahead[k] = t + k * step_t < nt && h + k * step_h < nh ? idx[k * idx_step] : 0;
     }
     uint4 raw[kUnroll][kRaw];
 #pragma unroll
@@ -170,23 +202,32 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int i = 0; i < kRaw; ++i) {
         raw[k][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (dst[k] >= 0 && j[k] >= 0) raw[k][i] = reinterpret_cast<const uint4*>(from[k])[i];
+        if (put[k] && from[k] != nullptr) raw[k][i] = reinterpret_cast<const uint4*>(from[k])[i];
       }
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      if (dst[k] < 0) continue;
+    for (int k = 0; k < kUnroll; ++k, o += o_step) {
+      if (!put[k]) continue;
       float y[16];
 #pragma unroll
-      for (int i = 0; i < kRaw; ++i) Vec16<T>::to_float(raw[k][i], y + i * (16 / kRaw));
-      const bool turn = rotate && g * 16 < plan.rot_dim;
+      for (int i = 0; i < kRaw; ++i) {
+        const uint32_t flip = sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
+        raw[k][i].x ^= flip;  // (rotation and maximum do not mind)
+        raw[k][i].y ^= flip;
+        raw[k][i].z ^= flip;
+        raw[k][i].w ^= flip;
+        Vec16<T>::to_float(raw[k][i], y + i * (16 / kRaw));
+      }
+      const bool turn = rotate && g * 16 < plan.rot_dim && from[k] != nullptr;
       if (turn) {
-        const float2* c = cs + ((r0 + k * kRowsPerPass) & (a.T - 1)) * half;
+        const float2* c = cs + (threadIdx.x / G & (a.T - 1)) * half;  // (by heads)
         if constexpr (kRope == 1) {
           const T* row = from[k] - g * 16;
           if (half % 16 == 0) {  // the group and its partners are whole groups
             float z[16];
             const bool low = g * 16 < half;
             load16(from[k] + (low ? half : -half), z);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = -z[i];
             c += low ? g * 16 : g * 16 - half;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -196,9 +237,9 @@ __global__ void __launch_bounds__(kThreads)
             for (int i = 0; i < 16; ++i) {
               const int e = g * 16 + i;
               if (e < half)
-                y[i] = rope_a(y[i], load1(row + e + half), c[e]);
+                y[i] = rope_a(y[i], -load1(row + e + half), c[e]);
               else if (e < plan.rot_dim)
-                y[i] = rope_b(load1(row + e - half), y[i], c[e - half]);
+                y[i] = rope_b(-load1(row + e - half), y[i], c[e - half]);
             }
           }
         } else if constexpr (kRope == 2) {
@@ -220,9 +261,8 @@ __global__ void __launch_bounds__(kThreads)
         amax = absmax16(y);
       uint32_t scale;
       const uint2 codes = quantise16(y, amax, down, up, scale);
-      const int64_t at = dst[k] * G + g;
-      reinterpret_cast<uint2*>(a.codes[kv])[at] = codes;
-      a.scales[kv][at] = (uint8_t)scale;
+      codes_out[o] = codes;
+      scales_out[o] = (uint8_t)scale;
     }
   }
 }
@@ -230,22 +270,22 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, int D>
 cudaError_t run_store(StoreArgs a, const fc_rope_plan* plan, cudaStream_t s) {
   constexpr int kRowsPerPass = kThreads / (D / 16);
-  constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
   // Rotated keys: few tokens and many heads to a block, which share the angles.
   // Otherwise a run of tokens, whose rows (or kept rows) lie close together.
-  const int most = plan != nullptr ? 3 : 7;
+  const int most = plan != nullptr ? 3 : 9;
   a.log_t = 0;
   while (a.log_t < most && (1 << a.log_t) < a.rows) ++a.log_t;
   a.T = 1 << a.log_t;
   a.n_lt = (int)ceil_div(a.rows, a.T);
+  // Heads of a block: with rotated keys as many as share the angles, unless that
+  // leaves SMs idle; else one, or what two loads of the block's threads reach.
   a.HG = a.H;
-  // the heads split while SMs would be idle, and without angles to share down to
-  // what a block's threads load at once
   const int64_t want = plan != nullptr ? 3ll * sm_count() : INT64_MAX;
   const int64_t tiles = (int64_t)a.N * a.n_lt;
-  const int least = plan != nullptr ? kRowsPerPass : kRowsPerPass * kUnroll;
+  const int least = plan != nullptr ? kRowsPerPass : 2 * kRowsPerPass;
   while (a.HG > 1 && tiles * ceil_div(a.H, a.HG) < want && (a.HG + 1) / 2 * a.T >= least)
     a.HG = (a.HG + 1) / 2;
+  if (a.T > kRowsPerPass) a.HG = 1;
   a.n_hg = (int)ceil_div(a.H, a.HG);
   const int64_t blocks = tiles * a.n_hg;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
