@@ -110,13 +110,13 @@ struct StoreArgs {
 
 // kRope: 0 none, 1 half layout, 2 interleaved.
 template <typename T, int D, int kRope>
-__global__ void __launch_bounds__(kThreads, kRope == 0 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, 4)
     store_kernel(const StoreArgs a, const __grid_constant__ fc_rope_plan plan) {
   extern __shared__ float2 cs[];  // [T][rot/2], behind the turns and the axes
   constexpr int G = D / 16;       // groups (and threads) of a row
   constexpr int kRowsPerPass = kThreads / G;
   constexpr int kRaw = (int)sizeof(T);  // 16-byte vectors of a group: 2 (bf16), 4
-  constexpr int kUnroll = 2;  // rows loaded before the first is stored
+  constexpr int kUnroll = kRope == 0 ? 2 : 1;  // rows loaded before the first is stored
   const int kv = blockIdx.y;  // 0 keys, 1 values
   int b = blockIdx.x;
   const int hg = b % a.n_hg;
