@@ -18,17 +18,19 @@ struct AttnArgs {
   const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
   int N, Hkv, G, R, Lq, max_len, cap;  // R = G * Lq rows of a key head
   int rows_blk, n_rb;                  // query rows of a block, row blocks of a key head
-  int n_split, chunk;
   bool stream;                         // shares of equal work (StreamShare)
+  int n_whole, n_split, chunk;         // without: units with a block of their own, blocks
+                                       // of each other one and their keys
   int blocks;                          // of the grid that computes
-  bool joined;                         // a second kernel follows
   bool causal;
   float scale_log2;  // scale * 2^k_exp * log2 e
   float out_scale;   // 2^v_exp
   int* err;
-  float2* part_ml;  // [N Hkv R][n_split] (log2 reference, sum); stream: [blocks][2][rows_blk]
-  float* part_o;    // [N Hkv R][n_split][d]; stream: [blocks][2][rows_blk][d]
-  int2* part_of;    // stream: [N Hkv][n_rb] (first block, blocks) of a unit
+  // what blocks that share a unit leave for the join: by block (stream: two slots to a
+  // block) and row
+  float2* part_ml;  // [..][rows_blk] (log2 reference, sum)
+  float* part_o;    // [..][rows_blk][d]
+  int2* part_of;    // [N Hkv][n_rb] (first block, blocks) of a unit
 };
 
 __device__ __forceinline__ int seq_len(const AttnArgs& a, int n) {
@@ -98,14 +100,20 @@ struct Piece {
   int n_parts;  // blocks that share the unit, where this one has its first stage
 };
 
-// A block's share, in shared memory (in registers it would stay through the loops
-// over stages).  begin() is called by the whole block, next() by one thread.
+// Where a walk through a share stands.
+struct Walk {
+  int64_t pos;    // work done
+  int64_t start;  // the work before entry e
+  int e;          // entry (sequence, row block) at pos
+};
+
+// A block's share, in shared memory.  begin() is called by the whole block.
 template <int kThreads>
 struct StreamShare {
   int64_t warp_sum[kThreads / 32];
-  int64_t total, pos, end;  // all work, the share's
-  int64_t start;            // the work before entry e
-  int C, e;                 // blocks, entry (sequence, row block) at pos
+  int64_t total, end;  // all work, the end of the share
+  int C;               // blocks
+  Walk first;
 
   __device__ __forceinline__ void begin(const AttnArgs& a, int least) {
     const int E = a.N * a.n_rb;
@@ -143,7 +151,7 @@ struct StreamShare {
       const int64_t lo = c < blocks ? div_small(all * c, blocks) : 0;
       const int64_t hi = c < blocks ? div_small(all * (c + 1), blocks) : 0;
       if (lo >= hi) {
-        if (threadIdx.x == 0) pos = end = 0;
+        if (threadIdx.x == 0) first.pos = end = 0;
       } else if (upto - own <= lo && lo < upto) {
         int64_t at = upto - own;
         int i = e0;
@@ -153,43 +161,57 @@ struct StreamShare {
           at += w;
         }
         total = all;
-        pos = lo;
         end = hi;
-        start = at;
         C = blocks;
-        e = i;
+        first.pos = lo;
+        first.start = at;
+        first.e = i;
       }
     }
     __syncthreads();
   }
 
   // The next piece with stages; false at the end of the share.
-  __device__ __forceinline__ bool next(const AttnArgs& a, Piece& p) {
-    while (pos < end) {
+  __device__ __forceinline__ bool next(const AttnArgs& a, Walk& at, Piece& p) const {
+    while (at.pos < end) {
       int w;
-      while ((w = entry_work(a, e)) == 0) ++e;
-      p.n = a.n_rb == 1 ? e : e / a.n_rb;
-      p.rb = e - p.n * a.n_rb;
+      while ((w = entry_work(a, at.e)) == 0) ++at.e;
+      p.n = a.n_rb == 1 ? at.e : at.e / a.n_rb;
+      p.rb = at.e - p.n * a.n_rb;
       p.n_unit = w - kUnitCost;
-      p.hk = (int)div_small(pos - start, w);
-      const int64_t unit0 = start + (int64_t)p.hk * w;
-      const int from = (int)(pos - unit0), to = (int)min((int64_t)w, from + (end - pos));
+      p.hk = (int)div_small(at.pos - at.start, w);
+      const int64_t unit0 = at.start + (int64_t)p.hk * w;
+      const int from = (int)(at.pos - unit0), to = (int)min((int64_t)w, from + (end - at.pos));
       p.s_begin = max(0, from - kUnitCost);
       p.s_end = max(0, to - kUnitCost);
       // the block with the unit's last stage: the largest c with T c / C <= it
       p.n_parts = 1;
       if (p.s_begin == 0 && p.s_end > 0 && p.s_end < p.n_unit)
         p.n_parts = (int)div_small((unit0 + w) * C - 1, total) - (int)blockIdx.x + 1;
-      pos += to - from;
+      at.pos += to - from;
       if (to == w && p.hk == a.Hkv - 1) {
-        start = pos;
-        ++e;
+        at.start = at.pos;
+        ++at.e;
       }
       if (p.s_end > p.s_begin) return true;
     }
     return false;
   }
 };
+// Without shares: unit i, by sequence, key head and row block, the last rows first
+// (where the mask is causal they see the most keys).
+__device__ __forceinline__ void unit_at(const AttnArgs& a, int64_t i, int& n, int& hk, int& rb) {
+  const int unit = (int)(i / a.n_rb);
+  rb = a.n_rb - 1 - (int)(i - (int64_t)unit * a.n_rb);
+  n = unit / a.Hkv;
+  hk = unit - n * a.Hkv;
+}
+__device__ __forceinline__ void whole_unit(const AttnArgs& a, Piece& p) {
+  unit_at(a, blockIdx.x, p.n, p.hk, p.rb);
+  p.s_begin = 0;
+  p.s_end = p.n_unit = entry_stages(a, p.n * a.n_rb + p.rb);
+  p.n_parts = 1;
+}
 
 // Four outputs of row r from their weighted sums o, the row's log2 reference
 // and its sum L of 2^(x - ref).

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     tc::fence_barrier_init();
   }
   grid_dep_wait();
-  if (a.joined) grid_dep_launch();
+  if (a.stream) grid_dep_launch();  // the join
 
   // The block's share: one unit, or a run of stages over units.
   if (a.stream) share.begin(a, kLeastStages);
@@ -161,16 +161,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   int base = 0;  // stages of the units before: slots and phases go on
   for (;;) {
   if (threadIdx.x == 0) {
-    if (a.stream) {
-      if (!share.next(a, piece)) piece.n_unit = -1;
-    } else {
-      const int unit = blockIdx.x / a.n_rb;
-      piece.n = unit / a.Hkv;
-      piece.hk = unit % a.Hkv;
-      piece.rb = blockIdx.x % a.n_rb;
-      piece.s_begin = 0;
-      piece.s_end = piece.n_unit = entry_stages(a, piece.n * a.n_rb + piece.rb);
-    }
+    if (!a.stream)
+      whole_unit(a, piece);
+    else if (!share.next(a, share.first, piece))
+      piece.n_unit = -1;
   }
   __syncthreads();
   if (piece.n_unit < 0) return;
@@ -601,37 +595,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
   __shared__ float part_l[kJoinWarps];
   const int lane = threadIdx.x & 31;
   const int warp = kRowWarps == 1 ? 0 : threadIdx.x >> 5;
-  const int64_t row = kRowWarps == 1 ? (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5)
-                                     : blockIdx.x;  // unit * R + r
-  if (row >= (int64_t)a.N * a.Hkv * a.R) return;
-  const int unit = (int)(row / a.R), r = (int)(row % a.R);
-  const int n = unit / a.Hkv, hk = unit % a.Hkv;
+  // rows of the units that blocks share
+  const int64_t i = kRowWarps == 1 ? (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t at_unit = i / a.rows_blk;
+  if (a.n_whole + at_unit >= (int64_t)a.N * a.Hkv * a.n_rb) return;
+  int n, hk, rb;
+  unit_at(a, a.n_whole + at_unit, n, hk, rb);
+  const int in_blk = (int)(i - at_unit * a.rows_blk), r = rb * a.rows_blk + in_blk;
+  if (r >= a.R) return;
   // Lengths are older than the kernel that this one depends on, which waited for
   // them itself before it let this one start.
-  const int len = seq_len(a, n);
-  const int rb = r / a.rows_blk;
-  const int k_top = block_keys(a, len, rb * a.rows_blk, a.rows_blk);
-  int ns = (k_top + a.chunk - 1) / a.chunk;
+  const bool some = entry_stages(a, n * a.n_rb + rb) > 0;
   const bool col = lane < D / 4;
-  const float2* ml = a.part_ml + row * a.n_split;
-  const float4* po = reinterpret_cast<const float4*>(a.part_o + row * a.n_split * D) + lane;
-  int step = 1;  // rows between parts
   grid_dep_wait();
-  if (a.stream) {
-    ns = 0;
-    if (k_top > 0) {
-      const int2 of = a.part_of[(int64_t)unit * a.n_rb + rb];
-      if (of.y == 1) return;  // one block had it all
-      ns = of.y;
-      // slot 1 of the first block, slot 0 of the others: two slots apart but for the
-      // first pair, which lie side by side
-      const int64_t first = ((int64_t)of.x * 2 + 1) * a.rows_blk + r % a.rows_blk;
-      ml = a.part_ml + first;
-      po += (first - row * a.n_split) * (D / 4);
-      step = a.rows_blk;
-    }
-  }
-  auto place = [&](int s) { return (int64_t)(a.stream && s > 0 ? 2 * s - 1 : s) * step; };
+  // (a share of equal work has no block for a unit without keys)
+  int2 of = make_int2(0, 0);
+  if (some || !a.stream) of = a.part_of[(int64_t)(n * a.Hkv + hk) * a.n_rb + rb];
+  if (of.y == 1) return;  // one block had it all
+  const int ns = of.y;
+  // of equal shares: slot 1 of the first block, slot 0 of the others
+  const int64_t at0 = (a.stream ? (int64_t)of.x * 2 + 1 : of.x) * a.rows_blk + in_blk;
+  const float2* ml = a.part_ml + at0;
+  const float4* po = reinterpret_cast<const float4*>(a.part_o + at0 * D) + lane;
+  auto place = [&](int s) { return (int64_t)(a.stream && s > 0 ? 2 * s - 1 : s) * a.rows_blk; };
   float2 x[kAhead];
   float4 v[kAhead];
 #pragma unroll
@@ -673,28 +659,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
   if (col) write_row<T>(a, n, hk, r, lane * 4, o, M, L);
 }
 
-// Shares of the key axis: enough blocks to fill the SMs, at least `least` keys to
-// a share.  With as many units as slots, or one short history, there is nothing to
-// split and the join is not launched.  n_most bounds n_split and does not fall
-// with max_len: the workspace goes by it, so one made for a length serves every
-// shorter one.
-struct Shares {
-  int n_split, chunk;
-  int64_t n_most;
-};
-Shares choose_split(int64_t units, int max_len, int64_t slots, int least) {
-  Shares s = {1, max_len > 0 ? (int)align_up((size_t)max_len, 128) : 128, 1};
-  if (max_len <= 2 * least || units >= slots) return s;
-  const int64_t want = slots / units;
-  if (want <= 1) return s;
-  const int64_t c = ceil_div(max_len, want);
-  s.chunk = (int)align_up((size_t)(c < least ? least : c), 128);
-  s.n_split = (int)ceil_div(max_len, s.chunk);
-  s.n_most = ceil_div(max_len, least);
-  if (s.n_most > want) s.n_most = want;
-  return s;
-}
-
 template <typename T, int D, int NR>
 cudaError_t run(const AttnArgs& a, int N, cudaStream_t s) {
   constexpr int smem = smem_bytes<D, NR>();
@@ -717,9 +681,8 @@ cudaError_t run(const AttnArgs& a, int N, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
-  const int64_t rows = (int64_t)N * a.Hkv * a.R;
-  // parts of a row: of equal shares, about the blocks to a unit
-  const int64_t parts = a.stream ? a.blocks / ((int64_t)N * a.Hkv * a.n_rb) + 2 : a.n_split;
+  const int64_t units = (int64_t)N * a.Hkv * a.n_rb, rows = (units - a.n_whole) * a.rows_blk;
+  const int64_t parts = a.stream ? a.blocks / units + 2 : a.n_split;  // of a row, about
   const bool one = parts <= 5;
   const int64_t blocks = one ? ceil_div(rows, kJoinWarps) : rows;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -741,43 +704,69 @@ cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
 bool use_tc(bool bf16, int R) { return bf16 && R > 16; }
 
 struct Layout {
-  int rows_blk, n_rb, n_split, chunk, blocks;
+  int rows_blk, n_rb, blocks, n_whole, n_split, chunk;
   bool stream;
   size_t of, ml, o, total;
 };
-bool layout(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d, Layout& l) {
+// causal: only for the choice of parts (the workspace does not go by it).
+bool layout(bool bf16, bool causal, int N, int Hq, int Hkv, int Lq, int max_len, int d, Layout& l) {
   const int R = Hq / Hkv * Lq;
   const bool tc = use_tc(bf16, R);
   l.rows_blk = tc ? kTcRows : R > 8 ? 16 : 8;
   l.n_rb = (int)ceil_div(R, l.rows_blk);
-  const int64_t units = (int64_t)N * Hkv * l.n_rb;
-  l.n_split = 1;
-  l.chunk = 1;
+  const int64_t units = (int64_t)N * Hkv * l.n_rb, sms = sm_count();
   l.stream = false;
-  size_t parts = 0;
-  int64_t blocks;
+  l.n_split = l.chunk = 1;
+  int64_t blocks = units, n_whole = units, parts = 0;
   if (tc) {
-    const Shares sh = choose_split(units, max_len, sm_count(), 512);
-    l.n_split = sh.n_split;
-    l.chunk = sh.chunk;
-    blocks = units * l.n_split;
-    parts = sh.n_most > 1 ? (size_t)N * Hkv * R * sh.n_most : 0;
+    // One block to an SM.  Whole waves of units have a block each; those of the last
+    // wave are split along the keys into s parts, with s such that the parts' own
+    // waves take least, counted in key tiles: a part costs about 4 beside its own, the
+    // join 6, and a causal unit has half of the longest's on average.  At most three
+    // waves of parts, of 512 keys or more.  (384 units of 160 tiles: 1108 us without,
+    // 1047 with; 192 causal units of up to 16: 41 without, 48 with.)
+    const int64_t rem = units % sms;
+    const int64_t tiles = ceil_div(max_len, kTcKeys);
+    int64_t most = rem > 0 ? 3 * sms / rem : 1;
+    if (most > max_len / 512) most = max_len / 512;
+    int64_t best = INT64_MAX, s = 1;
+    for (int64_t x = 1; x <= most || x == 1; ++x) {
+      const int64_t own = ceil_div(causal ? ceil_div(tiles, 2) : tiles, x);
+      const int64_t cost = ceil_div(rem * x, sms) * (own + 4) + (x > 1 ? 6 : 0);
+      if (cost < best) {
+        best = cost;
+        s = x;
+      }
+    }
+    if (s > 1) {
+      l.chunk = (int)ceil_div(tiles, s) * kTcKeys;
+      l.n_split = (int)ceil_div(max_len, l.chunk);
+    }
+    if (l.n_split > 1) {
+      n_whole = units - rem;
+      blocks = n_whole + rem * l.n_split;
+    }
+    // (a workspace made for a longer history serves this one)
+    parts = most > 1 ? rem * most : 0;
   } else {
     // Shares of equal work for what fills the SMs a few times at most.  A short
     // history is done by one block for each unit without the join, and with many
     // units the order in which blocks come evens them out.
-    const int64_t slots = (bf16 || l.rows_blk == 8 ? 2ll : 1ll) * sm_count();
+    const int64_t slots = (bf16 || l.rows_blk == 8 ? 2 : 1) * sms;
     l.stream = max_len > 512 && units < 16 * slots;
-    blocks = l.stream ? slots : units;
-    // (a workspace made for a longer history serves this one)
-    if (units < 16 * slots && max_len > 512) parts = (size_t)slots * 2 * l.rows_blk;
+    if (l.stream) {
+      blocks = slots;
+      n_whole = 0;
+      parts = slots * 2;
+    }
   }
   if (blocks > 0x7fffffffll) return false;
   l.blocks = (int)blocks;
+  l.n_whole = (int)n_whole;
   l.of = 256;
-  l.ml = align_up(l.of + (parts > 0 && !tc ? (size_t)units * sizeof(int2) : 0), 256);
-  l.o = align_up(l.ml + parts * sizeof(float2), 256);
-  l.total = align_up(l.o + parts * d * sizeof(float), 256);
+  l.ml = align_up(l.of + (parts > 0 ? (size_t)units * sizeof(int2) : 0), 256);
+  l.o = align_up(l.ml + (size_t)parts * l.rows_blk * sizeof(float2), 256);
+  l.total = align_up(l.o + (size_t)parts * l.rows_blk * d * sizeof(float), 256);
   return true;
 }
 
@@ -790,14 +779,14 @@ cudaError_t run_all(const AttnArgs& a, bool bf16, int N, cudaStream_t s) {
     e = bf16 ? run<__nv_bfloat16, D, 1>(a, N, s) : run<float, D, 1>(a, N, s);
   else
     e = bf16 ? run<__nv_bfloat16, D, 2>(a, N, s) : run<float, D, 2>(a, N, s);
-  if (e != cudaSuccess || !a.joined) return e;
+  if (e != cudaSuccess || (!a.stream && a.n_split == 1)) return e;
   return bf16 ? join<__nv_bfloat16, D>(a, N, s) : join<float, D>(a, N, s);
 }
 }  // namespace
 
 size_t kv4_attention_ws_bytes(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d) {
   Layout l;
-  return layout(bf16, N, Hq, Hkv, Lq, max_len, d, l) ? l.total : 0;
+  return layout(bf16, false, N, Hq, Hkv, Lq, max_len, d, l) ? l.total : 0;
 }
 
 cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* ws,
@@ -824,13 +813,13 @@ cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* 
   a.scale_log2 = ldexpf(p.scale * 1.4426950408889634f, c.k_exp);
   a.out_scale = ldexpf(1.0f, c.v_exp);
   Layout l;
-  if (!layout(p.bf16, c.N, p.Hq, c.H, p.Lq, p.max_len, c.d, l)) return cudaErrorInvalidValue;
+  if (!layout(p.bf16, p.causal, c.N, p.Hq, c.H, p.Lq, p.max_len, c.d, l)) return cudaErrorInvalidValue;
   a.rows_blk = l.rows_blk;
   a.n_rb = l.n_rb;
+  a.stream = l.stream;
+  a.n_whole = l.n_whole;
   a.n_split = l.n_split;
   a.chunk = l.chunk;
-  a.stream = l.stream;
-  a.joined = l.stream || l.n_split > 1;
   a.blocks = l.blocks;
   char* w = static_cast<char*>(ws);
   a.err = reinterpret_cast<int*>(w);

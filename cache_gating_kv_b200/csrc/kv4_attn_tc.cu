@@ -94,12 +94,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
   Bars* bars = reinterpret_cast<Bars*>(sCode + kCodes * kCode);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  int b = blockIdx.x;
-  const int split = b % a.n_split;
-  b /= a.n_split;
-  const int rb = a.causal ? a.n_rb - 1 - b % a.n_rb : b % a.n_rb;  // the longest first
-  const int unit = b / a.n_rb;
-  const int n = unit / a.Hkv, hk = unit % a.Hkv;
+  // The first n_whole units have a block each, the others n_split.
+  const int b = blockIdx.x, part = b - a.n_whole;
+  const bool shared_unit = part >= 0;
+  const int split = shared_unit ? part % a.n_split : 0;
+  int n, hk, rb;
+  unit_at(a, shared_unit ? a.n_whole + part / a.n_split : b, n, hk, rb);
+  const int unit = n * a.Hkv + hk;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCodes; ++i) {
@@ -125,23 +126,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_slot;
   grid_dep_wait();
-  if (a.joined) grid_dep_launch();
+  if (a.n_split > 1) grid_dep_launch();  // the join
 
   const int len = seq_len(a, n);
   const int r_base = rb * kTcRows;
-  const int k_begin = split * a.chunk;
+  const int chunk = shared_unit ? a.chunk : a.max_len;
+  const int k_begin = split * chunk;
   // keys and key tiles of each query tile
   int k_end[2], nt[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int r0 = r_base + j * kM;
-    k_end[j] = r0 < a.R ? min(block_keys(a, len, r0, kM), k_begin + a.chunk) : 0;
+    k_end[j] = r0 < a.R ? min(block_keys(a, len, r0, kM), k_begin + chunk) : 0;
     nt[j] = k_end[j] > k_begin ? (k_end[j] - k_begin + kN - 1) / kN : 0;
   }
   const int T = max(nt[0], nt[1]);
   const int k_top = max(k_end[0], k_end[1]);
-  // A share that the whole block does not need is not written: the join knows.
-  const bool idle = a.n_split > 1 && T == 0;
+  // The unit is joined from its parts if it has more than one with keys; parts without
+  // are not written.
+  const int keys = block_keys(a, len, r_base, kTcRows);
+  const int n_parts = shared_unit ? max(1, (keys + chunk - 1) / chunk) : 1;
+  const bool idle = split >= n_parts;
+  if (shared_unit && split == 0 && threadIdx.x == 0)
+    a.part_of[(int64_t)unit * a.n_rb + rb] = make_int2(part, n_parts);
   const int64_t head = (int64_t)unit * a.cap;
   bool ok = true;
 
@@ -269,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     if (!idle) {
       const float L = ref == -INFINITY ? 0.0f : l2.x + l2.y;
       const float at_ref = ref == -INFINITY ? ref : ref - kShift;
-      const int64_t at = ((int64_t)unit * a.R + r) * a.n_split + split;
-      if (a.n_split > 1 && have) a.part_ml[at] = make_float2(at_ref, L);
+      const int64_t at = (int64_t)part * kTcRows + j * kM + rloc;
+      if (n_parts > 1 && have) a.part_ml[at] = make_float2(at_ref, L);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
           for (int e = 0; e < 32; e += 4) {
             const float4 v = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
                                          __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-            if (a.n_split > 1)
+            if (n_parts > 1)
               *reinterpret_cast<float4*>(a.part_o + at * D + c * 32 + e) = v;
             else
               write_row<__nv_bfloat16>(a, n, hk, r, c * 32 + e, v, at_ref, L);
