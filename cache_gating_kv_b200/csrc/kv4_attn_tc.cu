@@ -45,7 +45,7 @@ constexpr int kCodes = 3;     // code stages
 constexpr float kShift = 5.0f, kSlack = 8.0f;
 // Registers of the softmax, converting and remaining warps; their sum over 512
 // threads is within the 65,536 that 512 x 128 at launch hold.
-constexpr int kRegSoftmax = 192, kRegConvert = 80, kRegRest = 40;
+constexpr int kRegSoftmax = 200, kRegConvert = 56, kRegRest = 48;
 static_assert(256 * kRegSoftmax + 128 * kRegConvert + 128 * kRegRest <= 512 * 128, "registers");
 
 template <int D> constexpr int op_bytes() { return kN * D * 2; }
@@ -69,6 +69,8 @@ static_assert(sizeof(Bars) <= kBarBytes, "barriers");
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (uint32_t)((c >> 3) * (kN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
+
+template <int J> struct Tile { static constexpr int value = J; };
 
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -386,47 +388,60 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       for (int x = max(0, h - kCodes); x < h; ++x)  // no copy outlives the block
         ok &= tc::mbar_wait(&bars->code_full[x % kCodes], (x / kCodes) & 1);
     } else if (warp == 13 && lane == 0 && T > 0) {
-      // ---- MMA issue
-      const uint32_t q_addr = tc::smem_u32(sQ), op_addr = tc::smem_u32(sOp);
-      auto qk = [&](int j, int os) {
+      // ---- MMA issue.  The logits of a tile wait for this thread twice a step, so it
+      // keeps no arrays and finds its descriptors by additions.
+      const uint64_t q_desc = tc::desc_k_sw128(tc::smem_u32(sQ));
+      const uint64_t k_desc = tc::desc_k_sw128(tc::smem_u32(sOp));
+      const uint64_t v_desc = tc::desc_mn_sw128(tc::smem_u32(sOp), kN * 128);
+      auto qk = [&](auto jc, int os) {
+        constexpr int j = decltype(jc)::value;
+        const uint64_t q = q_desc + j * (kQ >> 4), k = k_desc + os * (kOp >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * (kN * 128) + (kk & 3) * 32;
-          tc::mma_bf16(tmem + j * kN, tc::desc_k_sw128(q_addr + j * kQ + o),
-                       tc::desc_k_sw128(op_addr + os * kOp + o), kIdescQK, kk > 0 ? 1u : 0u);
+          const uint32_t o = ((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4;
+          tc::mma_bf16(tmem + j * kN, q + o, k + o, kIdescQK, kk > 0 ? 1u : 0u);
         }
         tc::mma_commit(&bars->s_full[j]);
       };
-      ok = tc::mbar_wait(&bars->q_full, 0) && tc::mbar_wait(&bars->op_full[0], 0);
+      auto pv = [&](auto jc, int os, int t) -> bool {
+        constexpr int j = decltype(jc)::value;
+        const uint64_t v = v_desc + os * (kOp >> 4);
+        if (!tc::mbar_wait(&bars->p_full[j], t & 1)) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < kN / 16; ++kk)
+          tc::mma_f16_ts(tmem + 2 * kN + j * D, tmem + j * kN + kk * 8, v + (kk * 2048 >> 4),
+                         kIdescPV, t > 0 || kk > 0 ? 1u : 0u);
+        return true;
+      };
+      auto stage_in = [&](int x) { return tc::mbar_wait(&bars->op_full[x % kOps], (x / kOps) & 1); };
+      constexpr Tile<0> t0;
+      constexpr Tile<1> t1;
+      const int nt0 = nt[0], nt1 = nt[1];
+      ok = tc::mbar_wait(&bars->q_full, 0) && stage_in(0);
       if (ok) {
         tc::fence_after_sync();
-        for (int j = 0; j < 2; ++j)
-          if (nt[j] > 0) qk(j, 0);
+        if (nt0 > 0) qk(t0, 0);
+        if (nt1 > 0) qk(t1, 0);
         tc::mma_commit(&bars->op_empty[0]);
       }
+#pragma unroll 1
       for (int t = 0; ok && t < T; ++t) {
-        const int hv = 2 * t + 1, hk1 = 2 * t + 2;
-        ok = tc::mbar_wait(&bars->op_full[hv % kOps], (hv / kOps) & 1);
-        for (int j = 0; ok && j < 2; ++j) {
-          if (t < nt[j]) {
-            if (!(ok = tc::mbar_wait(&bars->p_full[j], t & 1))) break;
-            tc::fence_after_sync();
-            const uint32_t v_addr = op_addr + (hv % kOps) * kOp;
-#pragma unroll
-            for (int kk = 0; kk < kN / 16; ++kk)
-              tc::mma_f16_ts(tmem + 2 * kN + j * D, tmem + j * kN + kk * 8,
-                             tc::desc_mn_sw128(v_addr + kk * 2048, kN * 128), kIdescPV,
-                             t > 0 || kk > 0 ? 1u : 0u);
-            if (t + 1 == nt[j]) tc::mma_commit(&bars->o_full[j]);
-          }
-          if (j == 1) tc::mma_commit(&bars->op_empty[hv % kOps]);
-          if (t + 1 < nt[j]) {
-            if (!(ok = tc::mbar_wait(&bars->op_full[hk1 % kOps], (hk1 / kOps) & 1))) break;
-            tc::fence_after_sync();
-            qk(j, hk1 % kOps);
-          }
+        const int sv = (2 * t + 1) % kOps, sk = (2 * t + 2) % kOps;
+        if (!(ok = stage_in(2 * t + 1))) break;
+        if (t + 1 < T && !(ok = stage_in(2 * t + 2))) break;
+        if (t < nt0) {
+          if (!(ok = pv(t0, sv, t))) break;
+          if (t + 1 == nt0) tc::mma_commit(&bars->o_full[0]);
         }
-        if (ok && t + 1 < T) tc::mma_commit(&bars->op_empty[hk1 % kOps]);
+        if (t + 1 < nt0) qk(t0, sk);
+        if (t < nt1) {
+          if (!(ok = pv(t1, sv, t))) break;
+          if (t + 1 == nt1) tc::mma_commit(&bars->o_full[1]);
+        }
+        tc::mma_commit(&bars->op_empty[sv]);
+        if (t + 1 < nt1) qk(t1, sk);
+        if (t + 1 < T) tc::mma_commit(&bars->op_empty[sk]);
       }
       if (!ok) {  // no MMA outlives the allocation
         tc::mma_commit(&bars->drained);

@@ -225,6 +225,7 @@ def _attend(q, c, lens, max_len=None, causal=False, scale=0.0, out=None, want_ls
     out = torch.full((N, Hq, Lq, d), 7.0, dtype=q.dtype, device=DEV) if out is None else out
     lse = torch.full((N, Hq, Lq), 7.0, device=DEV) if want_lse else None
     fc.fc_kv4_attention(q, c, lens, out, ws, max_len=max_len, causal=causal, scale=scale, lse=lse)
+    _attend.launches = fc.fc_last_launches()
     torch.cuda.synchronize()
     assert fc.fc_check_workspace(fc.FC_WS_IMPORTANCE, ws)
     return out, lse
@@ -409,6 +410,42 @@ def test_attention_far_offsets(Lq):
     k0, v0 = torch.empty_like(ko), torch.empty_like(vo)
     fc.fc_kv4_load(last, k0, v0, row0=0)
     assert torch.equal(ko, k0) and torch.equal(vo, v0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,Lq,lens,causal", [
+    (BF16, 3, 2, 2, 150, [2600, 130, 0], False), (BF16, 2, 4, 1, 40, [4090, 1700], True),
+    (BF16, 1, 3, 3, 300, [5000], True), (BF16, 2, 2, 1, 9, [6000, 3001], True),
+    (F32, 2, 2, 2, 70, [1500, 40], True), (F32, 1, 12, 1, 1, [3000], False)])
+def test_attention_long_axes_are_joined(dtype, N, Hq, Hkv, Lq, lens, causal, d):
+    """Units that several blocks share, in both kernels, beside short and empty ones."""
+    g = torch.Generator().manual_seed(57)
+    cap = (max(lens) + 15) // 16 * 16
+    c = _cache(g, N, Hkv, cap, d)
+    q = _randn(g, N, Hq, Lq, d).to(dtype).to(DEV)
+    out, lse = _attend(q, c, torch.tensor(lens, dtype=torch.int32, device=DEV), causal=causal)
+    assert _attend.launches == 2
+    _check(q, c, lens, out, lse, causal)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,Hkv", [(70, 3), (700, 8)])
+def test_attention_of_many_sequences(N, Hkv, dtype):
+    """More units than a block's threads add up at once, and more than are shared out."""
+    g = torch.Generator().manual_seed(59)
+    cap, d = 528, 64
+    c = fc.fc_kv4_cache(N, Hkv, cap, d)
+    for t in (c.k_codes, c.v_codes):
+        t.random_(0, 256)
+    for t in (c.k_scales, c.v_scales):
+        t.random_(0x28, 0x40)  # about a tenth to two
+    lens = torch.randint(0, cap + 1, (N,), generator=g, dtype=torch.int32)
+    lens[3], lens[5], lens[-1] = 0, cap, 1
+    q = _randn(g, N, 2 * Hkv, 1, d).to(dtype).to(DEV)
+    out, lse = _attend(q, c, lens.to(DEV))
+    some = [0, 3, 5, 41, N - 1]
+    few = fc.Kv4Cache(*[t[some].contiguous() for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales)])
+    _check(q[some], few, [int(lens[n]) for n in some], out[some], lse[some])
 
 
 def test_attention_refusals():
