@@ -73,7 +73,9 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // it ends the unit that an earlier block began, takes whole ones, and begins one.  A
 // unit whose stages several blocks share leaves one part for each, in slot 1 of the
 // block with its first stage and slot 0 of the others, and a second kernel joins
-// them.  The lengths are on the device, so every block adds up the work itself.
+// them.  The lengths are on the device, so every block adds up the work itself.  (32
+// sequences of unlike lengths, 8 key heads: 97 us with a unit cost of 0, 75 with 3; 82
+// with a fixed split of every unit.)
 constexpr int kStageKeys = 128;
 constexpr int kUnitCost = 3;
 

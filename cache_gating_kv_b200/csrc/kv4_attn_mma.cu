@@ -7,21 +7,31 @@
 // one pass over them: row r is query r / G of head r % G in the group.  The
 // bound is HBM: a key and its value are 144 bytes at d = 128 (72 at 64) for 4 R d
 // flops.  What has to keep up with it is the conversion of the codes, so
-//   - the codes go from shared memory straight into the B fragments of
-//     mma.m16n8k16 and are never written back as float16: a thread reads 32
-//     consecutive codes of a key (16 bytes), and the order in which the MMA
-//     steps see the elements of d is whatever that makes it, since the queries
-//     are loaded in the same order.  Values need pairs of keys instead of pairs
-//     of elements: two shift-and-select instructions interleave the nibbles of
-//     two keys' words before the conversion.  Which output column a thread's
-//     element is follows from the same freedom: each thread ends with 32
-//     consecutive outputs of a row;
+//   - keys and values are the A operand of mma.m16n8k16 and the rows its columns: up
+//     to 8 rows cost one n8 tile (as A operand, 16 whatever there are: twice the
+//     MMA, exponentials and accumulators; 110 -> 83 us for 32 sequences of up to
+//     16384 keys);
+//   - the codes go from shared memory straight into fragments and are never written
+//     back as float16: a thread reads 32 consecutive codes of a key (16 bytes), and
+//     the order in which the MMA steps see the elements of d is whatever that makes
+//     it, since the queries are stored in the same order.  Values need pairs of keys
+//     instead of pairs of elements: two shift-and-select instructions interleave the
+//     nibbles of two keys' words before the conversion;
 //   - code * scale is exact in float16 (at most 6 significant bits), so one
 //     packed multiplication per pair finishes the conversion;
-//   - each warp walks its own keys (steps of 32, in turn with the other warps of
-//     the block) behind its own ring of bulk copies, with its own running
-//     maximum, sum and output; there is no barrier in the loop.  The warps are
-//     joined at the end, and the shares of a long axis by a second, small kernel.
+//   - probabilities come out with keys on the rows and are wanted with keys on the K
+//     axis: one 8 x 8 transposition (movmatrix) for eight keys;
+//   - blocks of 8 warps take equal shares of all sequences' keys (StreamShare), in
+//     stages of 128 keys that bulk copies bring, four warps to a stage with 32 keys
+//     each and two stages at a time; a warp has its own running maximum, sum and
+//     output, so there is no barrier in the loop.  The logits of the next stage are
+//     computed beside the values of this one (81 -> 78 us).  The warps are joined at
+//     the end of a unit, and units that blocks share by a second, small kernel.
+// Per 32 keys a warp issues about 520 instructions, 128 of them conversions and 128
+// multiplications; at 16 warps an SM (120 registers; 24 warps of 80 spill and take
+// 92 us for 76) the schedulers issue in 3 of 5 cycles, which is what bounds it now:
+// 75 us for 312 MB (63 % of the measured copy rate), 37 us for one sequence of 131072
+// keys and 8 key heads (62 %); the same without any arithmetic takes 55 and 28.
 // The running maximum only moves when a step exceeds it by 2^8 (float16
 // probabilities, offset by 2^5, keep 11 bits over that range); for float32
 // queries it is exact, and queries and probabilities are sums of two float16
@@ -700,8 +710,11 @@ cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// The tcgen05 kernel takes over where the rows do not fit one pass of this one.
-bool use_tc(bool bf16, int R) { return bf16 && R > 16; }
+// The tcgen05 kernel computes 128 rows whatever there are, this one reads the keys
+// once more for every 16.  Measured at 128 key heads x 8192 keys: d = 128, 32 rows
+// 106 us here and 134 there, 48 rows 152 and 136; d = 64, 24 rows 59 and 112, and
+// 24 heads x 1000 keys with 64 rows 15 and 21.
+bool use_tc(bool bf16, int R, int d) { return bf16 && R > (d == 128 ? 32 : 64); }
 
 struct Layout {
   int rows_blk, n_rb, blocks, n_whole, n_split, chunk;
@@ -711,7 +724,7 @@ struct Layout {
 // causal: only for the choice of parts (the workspace does not go by it).
 bool layout(bool bf16, bool causal, int N, int Hq, int Hkv, int Lq, int max_len, int d, Layout& l) {
   const int R = Hq / Hkv * Lq;
-  const bool tc = use_tc(bf16, R);
+  const bool tc = use_tc(bf16, R, d);
   l.rows_blk = tc ? kTcRows : R > 8 ? 16 : 8;
   l.n_rb = (int)ceil_div(R, l.rows_blk);
   const int64_t units = (int64_t)N * Hkv * l.n_rb, sms = sm_count();

@@ -25,6 +25,15 @@
 // then the softmax warps scale O_j themselves: S_j of a tile is issued after
 // P_j V of the one before, so its arrival means that O_j is at rest.
 //
+// What bounds it: at N = 128 a tcgen05.mma with both operands in shared memory reads
+// 8 KB for 64 cycles of work, all that shared memory gives, and S_j -> P_j -> O_j is a
+// chain through three units.  4096 queries x 20480 keys x 24 heads, d = 128: 1.01-1.04
+// ms (0.63 ms at the measured GEMM rate); without exponentials, maximum and
+// conversion the schedule took 0.96 ms at a time when it took 1.12 with them.
+// Measured and not kept: a quarter of the exponentials on the FMA pipes (+5 %), P V
+// issued in halves (0), one read of S in two parts to save registers (+10 %), a
+// persistent loop over equal shares (+10 %: its state makes the softmax warps spill).
+//
 // Roles (512 threads): warps 0-3 and 4-7 softmax of tile 0 and 1 (a thread owns a
 // row), 8-11 conversion, 12 bulk copies, 13 MMA issue, 14 TMEM allocation.  Every
 // wait is bounded; one that gives up sets the workspace's error word.

@@ -6,7 +6,10 @@
 // angles are the only costly arithmetic (a float64 sine and cosine), and all
 // heads of a token share them.  A block therefore takes T tokens, writes their
 // T x rot/2 (c, s) pairs to shared memory once, and streams the rows of a
-// group of heads through them with 16-byte vectors.
+// group of heads through them with 16-byte vectors, a thread's pairs in registers.
+// 40 heads x 8190 tokens x 128 bf16: 31 us, 168 MB at 5.3 TB/s (82 % of the measured
+// copy rate); with frequencies read by lane from the constant bank 46, with 16
+// tokens to a block 33, with two rows in flight 34.
 #include "fc_common.cuh"
 #include "fc_kernels.h"
 #include "kv4.cuh"

@@ -7,8 +7,10 @@ reference implementation: the gate's Euler update equals torch's
 rows of the importance and the redundancy sum to one, the selection is
 ascending, in range and a top-B of the returned scores, the compaction equals
 ``index_select`` bitwise, the mask consumer round-trips, a cache commit keeps
-rows of its candidates, and no bounded device wait gave up.  Exits non-zero
-and names the first failed check.
+rows of its candidates, a rotation by zero changes nothing and its transpose
+undoes it, rows stored in 4 bits come back the same when stored again, attention
+over one key returns its value and over equal keys the mean of the values, and no
+bounded device wait gave up.  Exits non-zero and names the first failed check.
 """
 
 import sys
@@ -123,6 +125,39 @@ def run(device=0):
                                     for h in range(H)),
            "cache commit: a full buffer compresses to B_budget candidate rows")
     _check(fc.fc_check_workspace(fc.FC_WS_CACHE, cws), "cache commit: no bounded wait gave up")
+
+    # rotary positions, the 4-bit cache and its attention
+    plan = fc.fc_rope_init(d)
+    pos = torch.arange(Lk, dtype=torch.int32, device=dev)
+    kr, back = torch.empty(H, Lk, d, device=dev), torch.empty(H, Lk, d, device=dev)
+    fc.fc_rope(k.float(), kr, pos, plan)
+    fc.fc_rope(kr, back, pos, plan, inverse=True)
+    torch.cuda.synchronize()
+    _check(torch.equal(kr[:, 0], k[:, 0].float()) and
+           torch.allclose(back, k.float(), atol=1e-5), "rotation: position 0 and the transpose")
+    c4 = fc.fc_kv4_cache(1, H, 2000, d, device=dev)
+    fc.fc_kv4_store(k, vv, c4, rope=plan, pos=pos)
+    k1, v1 = torch.empty_like(k), torch.empty_like(k)
+    fc.fc_kv4_load(c4, k1, v1)
+    again = fc.fc_kv4_cache(1, H, 2000, d, device=dev)
+    fc.fc_kv4_store(k1, v1, again)
+    torch.cuda.synchronize()
+    _check(torch.equal(again.k_codes, c4.k_codes) and torch.equal(again.v_scales, c4.v_scales),
+           "4-bit rows: stored again, the same bits")
+    for rows in (1, 200):  # both attention kernels
+        qa = q[:, :rows].contiguous()
+        oa = torch.empty_like(qa)
+        wa = fc.workspace(fc.fc_kv4_attention_workspace_size(fc.FC_BF16, 1, H, H, rows, 2000, d), dev)
+        fc.fc_kv4_attention(qa, c4, 1, oa, wa)
+        torch.cuda.synchronize()
+        _check(torch.equal(oa, v1[:, :1].expand_as(oa)), f"4-bit attention, {rows} queries: one key")
+        same = fc.fc_kv4_cache(1, H, 2000, d, device=dev)
+        fc.fc_kv4_store(torch.zeros_like(k), vv, same)
+        fc.fc_kv4_attention(qa, same, 2000, oa, wa)
+        torch.cuda.synchronize()
+        _check(torch.allclose(oa.float(), v1.float().mean(1, keepdim=True).expand_as(oa), atol=1e-3),
+               f"4-bit attention, {rows} queries: equal keys give the mean")
+        _check(fc.fc_check_workspace(fc.FC_WS_IMPORTANCE, wa), "4-bit attention: no bounded wait gave up")
     print("selfcheck passed")
 
 
