@@ -359,12 +359,12 @@ def _rows(t, name):
     rows are contiguous; the other strides are free (None: dense)."""
     if not t.is_cuda:
         raise FlowCacheError("tensor arguments must be CUDA tensors")
-    shape = tuple(t.shape)
+    shape = t.shape
     n = len(shape)
     if n != 4:
         if n != 3:
             raise FlowCacheError(f"{name} must be [N, H, L, d] or [H, L, d]")
-        shape = (1,) + shape
+        shape = (1,) + tuple(shape)
     if t.is_contiguous():
         return t.data_ptr(), shape, None
     st = t.stride()
@@ -373,22 +373,19 @@ def _rows(t, name):
     return t.data_ptr(), shape, _I64x3(st[0] if n == 4 else 0, st[-3], st[-2])
 
 
-def _ints(t, shape, name):
-    """Pointer of a contiguous int32 CUDA tensor of the given number of elements."""
-    if t.dtype != torch.int32:
+def _ints(t, n, name):
+    """Pointer of a contiguous int32 CUDA tensor of n elements."""
+    if t.dtype is not torch.int32:
         raise FlowCacheError(f"{name} must be int32")
-    n = 1
-    for s in shape:
-        n *= s
     if t.numel() != n:
-        raise FlowCacheError(f"{name} has {t.numel()} elements, not {n} ({list(shape)})")
+        raise FlowCacheError(f"{name} has {t.numel()} elements, not {n}")
     return _p(t)
 
 
 def _first_row(row0, N):
     """(host row, device rows) of a ``row0`` argument."""
     if isinstance(row0, torch.Tensor):
-        return 0, _ints(row0, (N,), "row0")
+        return 0, _ints(row0, N, "row0")
     return int(row0), None
 
 
@@ -397,7 +394,7 @@ def _plan_args(rope, pos, N, L):
         return None, None
     if pos is None:
         raise FlowCacheError("a rotation needs pos")
-    return ctypes.byref(rope), _ints(pos, (rope.n_axes, N, L), "pos")
+    return ctypes.byref(rope), _ints(pos, rope.n_axes * N * L, "pos")
 
 
 def fc_rope_init(rot_dim, layout=FC_ROPE_HALF, base=10000.0, scaling=FC_ROPE_PLAIN, factor=1.0,
@@ -443,6 +440,7 @@ class Kv4Cache:
         self.N, self.H, self.cap, self.d = N, H, cap, 2 * half
         self.struct = _Kv4(_p(k_codes), _p(k_scales), _p(v_codes), _p(v_scales), N, H, cap, 2 * half,
                            int(k_exp), int(v_exp))
+        self._ref = ctypes.byref(self.struct)
 
 
 def fc_kv4_cache(N, H, cap, d, k_exp=0, v_exp=0, device=None):
@@ -464,8 +462,8 @@ def fc_kv4_store(k, v, cache, row0=0, idx=None, rope=None, pos=None, stream=None
     B = 0 if idx is None else idx.shape[-1]
     plan, p = _plan_args(rope, pos, N, L)
     st = library().fc_kv4_store(kp, vp, _dtype_code(k), N, H, L, d, ks, vs,
-                                 None if idx is None else _ints(idx, (N, H, B), "idx"), B, host, dev,
-                                 plan, p, ctypes.byref(cache.struct), _s(stream))
+                                 None if idx is None else _ints(idx, N * H * B, "idx"), B, host, dev,
+                                 plan, p, cache._ref, _s(stream))
     _check("fc_kv4_store", st)
 
 
@@ -477,7 +475,7 @@ def fc_kv4_load(cache, k_out, v_out, row0=0, stream=None):
     if vshape != (N, H, L, d) or v_out.dtype != k_out.dtype or (N, H, d) != (cache.N, cache.H, cache.d):
         raise FlowCacheError("k_out and v_out must be [N, H, L, d] of the cache, of one type")
     host, dev = _first_row(row0, N)
-    st = library().fc_kv4_load(ctypes.byref(cache.struct), kp, vp, _dtype_code(k_out), L, ks, vs, host,
+    st = library().fc_kv4_load(cache._ref, kp, vp, _dtype_code(k_out), L, ks, vs, host,
                                 dev, _s(stream))
     _check("fc_kv4_load", st)
 
@@ -500,12 +498,12 @@ def fc_kv4_attention(q, cache, lens, out, ws, max_len=None, causal=False, scale=
         max_len = cache.cap
     lp = None
     if isinstance(lens, torch.Tensor):
-        lp = _ints(lens, (N,), "lens")
+        lp = _ints(lens, N, "lens")
     elif lens is not None:
         max_len = min(int(lens), int(max_len))
     if lse is not None and (lse.dtype != torch.float32 or lse.numel() != N * Hq * Lq):
         raise FlowCacheError("lse must be [N, Hq, Lq] float32")
-    st = library().fc_kv4_attention(qp, ctypes.byref(cache.struct), lp, int(max_len), _dtype_code(q),
+    st = library().fc_kv4_attention(qp, cache._ref, lp, int(max_len), _dtype_code(q),
                                      N, Hq, Lq, d, qs, 1 if causal else 0, float(scale), op, os_,
                                      _p(lse), _p(ws), ws.numel() * ws.element_size(), _s(stream))
     _check("fc_kv4_attention", st)

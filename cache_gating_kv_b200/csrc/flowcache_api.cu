@@ -228,8 +228,9 @@ fc_status check_cache(const fc_kv4_cache* c, CacheSpans* out) {
     return fail(FC_ERR_INVALID_ARG, "cache: N, H must be >= 1 and N * H <= 2^20");
   if (c->d != 64 && c->d != 128)
     return fail(FC_ERR_UNSUPPORTED, "cache: d must be 64 or 128 (got %d)", c->d);
-  if (c->cap < 16 || c->cap % 16 != 0)
-    return fail(FC_ERR_INVALID_ARG, "cache: cap must be a multiple of 16 (got %d)", c->cap);
+  if (c->cap < 16 || c->cap % 16 != 0 || c->cap > (1 << 30))
+    return fail(FC_ERR_INVALID_ARG, "cache: cap must be a multiple of 16, at most 2^30 (got %d)",
+                c->cap);
   if (c->k_exp < -64 || c->k_exp > 64 || c->v_exp < -64 || c->v_exp > 64)
     return fail(FC_ERR_INVALID_ARG, "cache: k_exp and v_exp must be in [-64, 64]");
   FC_TRY(check_ptr_here(c->k_codes, "cache k_codes"));
@@ -255,7 +256,7 @@ const char* fc_last_error(void) { return g_err; }
 
 int fc_last_launches(void) { return fc::g_launches; }
 
-int fc_version(void) { return 100; }
+int fc_version(void) { return 200; }
 
 size_t fc_gate_workspace_size(int n_chunks, int64_t n_per_chunk) {
   (void)n_per_chunk;
@@ -773,7 +774,7 @@ size_t fc_kv4_attention_workspace_size(fc_dtype dtype, int N, int Hq, int Hkv, i
                                        int max_len, int d) {
   if ((dtype != FC_F32 && dtype != FC_BF16) || N < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 ||
       (int64_t)N * Hq > (1 << 20) || Lq < 1 || (int64_t)(Hq / Hkv) * Lq > INT32_MAX / 2 ||
-      max_len < 0 || (d != 64 && d != 128))
+      max_len < 0 || max_len > (1 << 30) || (d != 64 && d != 128))
     return 0;
   return fc::kv4_attention_ws_bytes(dtype == FC_BF16, N, Hq, Hkv, Lq, max_len, d);
 }

@@ -499,7 +499,7 @@ typedef struct {
   void* v_codes;
   void* v_scales;
   int32_t N, H;         /* sequences, key heads */
-  int32_t cap;          /* rows of a sequence; a multiple of 16 */
+  int32_t cap;          /* rows of a sequence; a multiple of 16, at most 2^30 */
   int32_t d;            /* 64 or 128 */
   int32_t k_exp, v_exp; /* in [-64, 64]: moves the scales' range, 2^-9 to 448 */
 } fc_kv4_cache;

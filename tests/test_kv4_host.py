@@ -100,6 +100,7 @@ def test_size_refusals_come_before_pointers():
     assert b"overlap" in lib.fc_last_error()
     assert lib.fc_kv4_load(None, None, None, 1, 1, None, None, 0, None, None) == 1
     for field, value, want in [("N", 0, 1), ("H", 0, 1), ("d", 96, 2), ("cap", 20, 1), ("cap", 0, 1),
+                               ("cap", (1 << 30) + 16, 1),
                                ("k_exp", 65, 1), ("v_exp", -65, 1)]:
         x = fc._Kv4(0, 0, 0, 0, 1, 1, 16, 64, 0, 0)
         setattr(x, field, value)
