@@ -721,8 +721,8 @@ struct Layout {
   bool stream;
   size_t of, ml, o, total;
 };
-// causal: only for the choice of parts (the workspace does not go by it).
-bool layout(bool bf16, bool causal, int N, int Hq, int Hkv, int Lq, int max_len, int d, Layout& l) {
+// causal, unlike: only for the choice of parts (the workspace does not go by them).
+bool layout(bool bf16, bool causal, bool unlike, int N, int Hq, int Hkv, int Lq, int max_len, int d, Layout& l) {
   const int R = Hq / Hkv * Lq;
   const bool tc = use_tc(bf16, R, d);
   l.rows_blk = tc ? kTcRows : R > 8 ? 16 : 8;
@@ -762,15 +762,23 @@ bool layout(bool bf16, bool causal, int N, int Hq, int Hkv, int Lq, int max_len,
     // (a workspace made for a longer history serves this one)
     parts = most > 1 ? rem * most : 0;
   } else {
-    // Shares of equal work for what fills the SMs a few times at most.  A short
-    // history is done by one block for each unit without the join, and with many
-    // units the order in which blocks come evens them out.
+    // Equal shares, or a block for each unit.  In stages (0.5 us each), with S of the
+    // longest unit and half of them on average where the lengths come from the device:
+    // blocks of their own take S in one wave, or all work and half of S in several;
+    // equal shares take all work, 3 for a unit (kUnitCost), and the join, 7 and one for
+    // 16 units.  Measured, own block / share, in us: 8 units of 768 keys 7.0 / 7.4, of
+    // 1024 8.1 / 7.5, of 4096 21 / 8.2; 64 units of 1536 keys 10.5 / 11.5, of 2048 12.9 /
+    // 12.3; 256 of 4096 33.9 / 37.3, but of up to 16384, half on average, 115 / 75.
     const int64_t slots = (bf16 || l.rows_blk == 8 ? 2 : 1) * sms;
-    l.stream = max_len > 512 && units < 16 * slots;
+    const bool may = max_len > 512 && units < 16 * slots;
+    const double S = (double)ceil_div(max_len, kStageKeys), mean = unlike ? 0.5 * S : S;
+    const double fill = (double)units / (double)slots;
+    const double own = units <= slots ? S : fill * mean + 0.5 * S;
+    l.stream = may && own > fill * (mean + 3.0) + 7.0 + (double)units / 16.0;
+    if (may) parts = slots * 2;
     if (l.stream) {
       blocks = slots;
       n_whole = 0;
-      parts = slots * 2;
     }
   }
   if (blocks > 0x7fffffffll) return false;
@@ -799,7 +807,7 @@ cudaError_t run_all(const AttnArgs& a, bool bf16, int N, cudaStream_t s) {
 
 size_t kv4_attention_ws_bytes(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d) {
   Layout l;
-  return layout(bf16, false, N, Hq, Hkv, Lq, max_len, d, l) ? l.total : 0;
+  return layout(bf16, false, false, N, Hq, Hkv, Lq, max_len, d, l) ? l.total : 0;
 }
 
 cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* ws,
@@ -826,7 +834,7 @@ cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* 
   a.scale_log2 = ldexpf(p.scale * 1.4426950408889634f, c.k_exp);
   a.out_scale = ldexpf(1.0f, c.v_exp);
   Layout l;
-  if (!layout(p.bf16, p.causal, c.N, p.Hq, c.H, p.Lq, p.max_len, c.d, l)) return cudaErrorInvalidValue;
+  if (!layout(p.bf16, p.causal, p.lens != nullptr, c.N, p.Hq, c.H, p.Lq, p.max_len, c.d, l)) return cudaErrorInvalidValue;
   a.rows_blk = l.rows_blk;
   a.n_rb = l.n_rb;
   a.stream = l.stream;
