@@ -79,6 +79,12 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (uint32_t)((c >> 3) * (kN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// One arrival for the warp, behind what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
 template <int J> struct Tile { static constexpr int value = J; };
 
 __device__ __forceinline__ void fence_async() {
@@ -116,16 +122,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCodes; ++i) {
       tc::mbar_init(&bars->code_full[i], 1);
-      tc::mbar_init(&bars->code_empty[i], 128);
+      tc::mbar_init(&bars->code_empty[i], 4);
     }
     for (int i = 0; i < kOps; ++i) {
-      tc::mbar_init(&bars->op_full[i], 128);
+      tc::mbar_init(&bars->op_full[i], 4);
       tc::mbar_init(&bars->op_empty[i], 1);
     }
-    tc::mbar_init(&bars->q_full, 256);
+    tc::mbar_init(&bars->q_full, 8);
     for (int j = 0; j < 2; ++j) {
       tc::mbar_init(&bars->s_full[j], 1);
-      tc::mbar_init(&bars->p_full[j], 128);
+      tc::mbar_init(&bars->p_full[j], 4);
       tc::mbar_init(&bars->o_full[j], 1);
     }
     tc::mbar_init(&bars->drained, 1);
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
                        pack_f16(f[4] * down, f[5] * down), pack_f16(f[6] * down, f[7] * down));
       }
       fence_async();
-      tc::mbar_arrive(&bars->q_full);
+      warp_arrive(&bars->q_full);
     }
     const int lim = have ? min(k_top, row_keys(a, len, i)) : k_top;  // keys of the row
     int lim_min = lim;
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       l2 = tc::fadd2(l2, sum);
       tc::tmem_st_wait();
       tc::fence_before_sync();
-      tc::mbar_arrive(&bars->p_full[j]);
+      warp_arrive(&bars->p_full[j]);
     }
     // ---- the row's result
     if (ok && nt[j] > 0) {
@@ -364,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
         }
       }
       fence_async();
-      tc::mbar_arrive(&bars->op_full[os]);
-      tc::mbar_arrive(&bars->code_empty[cs]);
+      warp_arrive(&bars->op_full[os]);
+      if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&bars->code_empty[cs]);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegRest));
