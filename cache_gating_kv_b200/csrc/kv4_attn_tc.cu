@@ -27,7 +27,7 @@
 //
 // What bounds it: at N = 128 a tcgen05.mma with both operands in shared memory reads
 // 8 KB for 64 cycles of work, all that shared memory gives, and S_j -> P_j -> O_j is a
-// chain through three units.  4096 queries x 20480 keys x 24 heads, d = 128: 1.01-1.04
+// chain through three units.  4096 queries x 20480 keys x 24 heads, d = 128: 1.00-1.04
 // ms (0.63 ms at the measured GEMM rate); without exponentials, maximum and
 // conversion the schedule took 0.96 ms at a time when it took 1.12 with them.
 // Measured and not kept: a quarter of the exponentials on the FMA pipes (+5 %), P V
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     float ref = -INFINITY;
     float2 l2 = make_float2(0.f, 0.f);
     for (int t = 0; t < nt[j]; ++t) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[j], t & 1))) {
+      if (!__all_sync(0xffffffffu, tc::mbar_sleep(&bars->s_full[j], t & 1))) {
         ok = false;
         break;
       }
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     }
     // ---- the row's result
     if (ok && nt[j] > 0) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->o_full[j], 0));
+      ok = __all_sync(0xffffffffu, tc::mbar_sleep(&bars->o_full[j], 0));
       tc::fence_after_sync();
     }
     if (!idle) {
@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     const int turn = (part >> 1) * 2;
     for (int h = 0; h < 2 * T; ++h) {
       const int cs = h % kCodes, os = h % kOps;
-      if (!tc::mbar_wait(&bars->code_full[cs], (h / kCodes) & 1) ||
-          !tc::mbar_wait(&bars->op_empty[os], ((h / kOps) & 1) ^ 1)) {
+      if (!tc::mbar_sleep(&bars->code_full[cs], (h / kCodes) & 1) ||
+          !tc::mbar_sleep(&bars->op_empty[os], ((h / kOps) & 1) ^ 1)) {
         ok = false;
         break;
       }
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       int h = 0;
       for (; h < 2 * T; ++h) {
         const int cs = h % kCodes;
-        if (!tc::mbar_wait(&bars->code_empty[cs], ((h / kCodes) & 1) ^ 1)) {
+        if (!tc::mbar_sleep(&bars->code_empty[cs], ((h / kCodes) & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
         }
       }
       for (int x = max(0, h - kCodes); x < h; ++x)  // no copy outlives the block
-        ok &= tc::mbar_wait(&bars->code_full[x % kCodes], (x / kCodes) & 1);
+        ok &= tc::mbar_sleep(&bars->code_full[x % kCodes], (x / kCodes) & 1);
     } else if (warp == 13 && lane == 0 && T > 0) {
       // ---- MMA issue.  The logits of a tile wait for this thread twice a step, so it
       // keeps no arrays and finds its descriptors by additions.
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       auto pv = [&](auto jc, int os, int t) -> bool {
         constexpr int j = decltype(jc)::value;
         const uint64_t v = v_desc + os * (kOp >> 4);
-        if (!tc::mbar_wait(&bars->p_full[j], t & 1)) return false;
+        if (!tc::mbar_sleep(&bars->p_full[j], t & 1)) return false;
         tc::fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < kN / 16; ++kk)
@@ -429,11 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
                          kIdescPV, t > 0 || kk > 0 ? 1u : 0u);
         return true;
       };
-      auto stage_in = [&](int x) { return tc::mbar_wait(&bars->op_full[x % kOps], (x / kOps) & 1); };
+      auto stage_in = [&](int x) { return tc::mbar_sleep(&bars->op_full[x % kOps], (x / kOps) & 1); };
       constexpr Tile<0> t0;
       constexpr Tile<1> t1;
       const int nt0 = nt[0], nt1 = nt[1];
-      ok = tc::mbar_wait(&bars->q_full, 0) && stage_in(0);
+      ok = tc::mbar_sleep(&bars->q_full, 0) && stage_in(0);
       if (ok) {
         tc::fence_after_sync();
         if (nt0 > 0) qk(t0, 0);
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       }
       if (!ok) {  // no MMA outlives the allocation
         tc::mma_commit(&bars->drained);
-        tc::mbar_wait(&bars->drained, 0);
+        tc::mbar_sleep(&bars->drained, 0);
       }
     }
   }
