@@ -27,12 +27,17 @@
 //
 // What bounds it: at N = 128 a tcgen05.mma with both operands in shared memory reads
 // 8 KB for 64 cycles of work, all that shared memory gives, and S_j -> P_j -> O_j is a
-// chain through three units.  4096 queries x 20480 keys x 24 heads, d = 128: 1.00-1.04
-// ms (0.63 ms at the measured GEMM rate); without exponentials, maximum and
-// conversion the schedule took 0.96 ms at a time when it took 1.12 with them.
-// Measured and not kept: a quarter of the exponentials on the FMA pipes (+5 %), P V
-// issued in halves (0), one read of S in two parts to save registers (+10 %), a
-// persistent loop over equal shares (+10 %: its state makes the softmax warps spill).
+// chain through three units.  4096 queries x 20480 keys x 24 heads, d = 128: 0.97-1.0
+// ms (0.63 ms at the measured GEMM rate).  In clocks a tile of 128 keys takes a softmax
+// warp 3700: 200 for the load, 470 for the maximum, 1400 for the exponentials (1024 at
+// the units' rate), 100 for the store and 1500 of waiting, in which the tensor cores
+// have 500 of P V and 700 of Q K^T for each of the two query tiles.  So P goes out in
+// halves, and P V starts behind the first (972 us for 988).
+// Measured and not kept: a quarter of the exponentials on the FMA pipes (+5 %), one
+// read of S in two parts to save registers (+10 %), a persistent loop over equal shares
+// (+10 %: its state makes the softmax warps spill), S in halves of 64 keys computed one
+// ahead (+10 %: at N = 64 the tensor cores take 90 clocks for 16 of K in P V, 64 in
+// Q K^T), six converting warps (0).
 //
 // Roles (512 threads): warps 0-3 and 4-7 softmax of tile 0 and 1 (a thread owns a
 // row), 8-11 conversion, 12 bulk copies, 13 MMA issue, 14 TMEM allocation.  Every
@@ -68,7 +73,7 @@ struct Bars {
   uint64_t code_full[kCodes], code_empty[kCodes];
   uint64_t op_full[kOps], op_empty[kOps];
   uint64_t q_full;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];  // of the query tiles; P in halves
   uint64_t drained;
   uint32_t tmem_slot;
 };
@@ -131,7 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     tc::mbar_init(&bars->q_full, 8);
     for (int j = 0; j < 2; ++j) {
       tc::mbar_init(&bars->s_full[j], 1);
-      tc::mbar_init(&bars->p_full[j], 4);
+      tc::mbar_init(&bars->p_full[j][0], 4);
+      tc::mbar_init(&bars->p_full[j][1], 4);
       tc::mbar_init(&bars->o_full[j], 1);
     }
     tc::mbar_init(&bars->drained, 1);
@@ -141,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = bars->tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_slot, 0);  // known as uniform
   grid_dep_wait();
   if (a.n_split > 1) grid_dep_launch();  // the join
 
@@ -267,23 +273,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       const float off = kShift - (ref == -INFINITY ? 0.0f : ref);
       const float2 ff = make_float2(fac, fac), oo = make_float2(off, off);
       float2 sum = make_float2(0.f, 0.f);
-      uint32_t p[64];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int hp = 0; hp < 2; ++hp) {
+        uint32_t p[32];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = tc::ffma2(f2(s[c][2 * e], s[c][2 * e + 1]), ff, oo);
-          const float2 y = make_float2(tc::ex2(x.x), tc::ex2(x.y));
-          sum = tc::fadd2(sum, y);
-          p[c * 16 + e] = pack_f16(y.x, y.y);
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t* v = s[2 * hp + c] + 2 * e;
+            const float2 x = tc::ffma2(f2(v[0], v[1]), ff, oo);
+            const float2 y = make_float2(tc::ex2(x.x), tc::ex2(x.y));
+            sum = tc::fadd2(sum, y);
+            p[c * 16 + e] = pack_f16(y.x, y.y);
+          }
         }
+        tc::tmem_st32(tS + hp * 32, p);
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        warp_arrive(&bars->p_full[j][hp]);
       }
-      tc::tmem_st32(tS, p);
-      tc::tmem_st32(tS + 32, p + 32);
       l2 = tc::fadd2(l2, sum);
-      tc::tmem_st_wait();
-      tc::fence_before_sync();
-      warp_arrive(&bars->p_full[j]);
     }
     // ---- the row's result
     if (ok && nt[j] > 0) {
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       const uint8_t* scales = codes + kN * CB;
       uint8_t* op = sOp + os * kOp;
       const int left = k_top - (k_begin + (h >> 1) * kN);
-#pragma unroll 2
+#pragma unroll 1
       for (int p = 0; p < kN / kPass; ++p) {
         const int r = p * kPass + r0;
         const uint4 w = *reinterpret_cast<const uint4*>(codes + r * CB + part * 16);
@@ -402,15 +411,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       }
       for (int x = max(0, h - kCodes); x < h; ++x)  // no copy outlives the block
         ok &= tc::mbar_sleep(&bars->code_full[x % kCodes], (x / kCodes) & 1);
-    } else if (warp == 13 && lane == 0 && T > 0) {
-      // ---- MMA issue.  The logits of a tile wait for this thread twice a step, so it
-      // keeps no arrays and finds its descriptors by additions.
+    } else if (warp == 13 && T > 0) {
+      // ---- MMA issue.  The logits of a tile wait for this warp twice a step, so it
+      // keeps no arrays and finds its descriptors by additions.  The warp stays together
+      // and one elected thread issues: with the loop in a single thread of a divergent
+      // warp an MMA took some 120 clocks to issue (1013 us for 996; 40.5 for 38.6 for 4
+      // causal prompts).
       const uint64_t q_desc = tc::desc_k_sw128(tc::smem_u32(sQ));
       const uint64_t k_desc = tc::desc_k_sw128(tc::smem_u32(sOp));
       const uint64_t v_desc = tc::desc_mn_sw128(tc::smem_u32(sOp), kN * 128);
+      auto wait = [&](uint64_t* bar, int phase) {
+        return __all_sync(0xffffffffu, tc::mbar_sleep(bar, phase & 1)) != 0;
+      };
       auto qk = [&](auto jc, int os) {
         constexpr int j = decltype(jc)::value;
         const uint64_t q = q_desc + j * (kQ >> 4), k = k_desc + os * (kOp >> 4);
+        if (!tc::elect()) return;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = ((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4;
@@ -421,24 +437,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       auto pv = [&](auto jc, int os, int t) -> bool {
         constexpr int j = decltype(jc)::value;
         const uint64_t v = v_desc + os * (kOp >> 4);
-        if (!tc::mbar_sleep(&bars->p_full[j], t & 1)) return false;
-        tc::fence_after_sync();
 #pragma unroll
-        for (int kk = 0; kk < kN / 16; ++kk)
-          tc::mma_f16_ts(tmem + 2 * kN + j * D, tmem + j * kN + kk * 8, v + (kk * 2048 >> 4),
-                         kIdescPV, t > 0 || kk > 0 ? 1u : 0u);
+        for (int hp = 0; hp < 2; ++hp) {
+          if (!wait(&bars->p_full[j][hp], t)) return false;
+          tc::fence_after_sync();
+          if (tc::elect()) {
+#pragma unroll
+            for (int kk = hp * kN / 32; kk < (hp + 1) * kN / 32; ++kk)
+              tc::mma_f16_ts(tmem + 2 * kN + j * D, tmem + j * kN + kk * 8, v + (kk * 2048 >> 4),
+                             kIdescPV, t > 0 || kk > 0 ? 1u : 0u);
+          }
+        }
         return true;
       };
-      auto stage_in = [&](int x) { return tc::mbar_sleep(&bars->op_full[x % kOps], (x / kOps) & 1); };
+      auto stage_in = [&](int x) { return wait(&bars->op_full[x % kOps], x / kOps); };
+      auto commit = [&](uint64_t* bar) {
+        if (tc::elect()) tc::mma_commit(bar);
+      };
       constexpr Tile<0> t0;
       constexpr Tile<1> t1;
       const int nt0 = nt[0], nt1 = nt[1];
-      ok = tc::mbar_sleep(&bars->q_full, 0) && stage_in(0);
+      ok = wait(&bars->q_full, 0) && stage_in(0);
       if (ok) {
         tc::fence_after_sync();
         if (nt0 > 0) qk(t0, 0);
         if (nt1 > 0) qk(t1, 0);
-        tc::mma_commit(&bars->op_empty[0]);
+        commit(&bars->op_empty[0]);
       }
 #pragma unroll 1
       for (int t = 0; ok && t < T; ++t) {
@@ -447,20 +471,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
         if (t + 1 < T && !(ok = stage_in(2 * t + 2))) break;
         if (t < nt0) {
           if (!(ok = pv(t0, sv, t))) break;
-          if (t + 1 == nt0) tc::mma_commit(&bars->o_full[0]);
+          if (t + 1 == nt0) commit(&bars->o_full[0]);
         }
         if (t + 1 < nt0) qk(t0, sk);
         if (t < nt1) {
           if (!(ok = pv(t1, sv, t))) break;
-          if (t + 1 == nt1) tc::mma_commit(&bars->o_full[1]);
+          if (t + 1 == nt1) commit(&bars->o_full[1]);
         }
-        tc::mma_commit(&bars->op_empty[sv]);
+        commit(&bars->op_empty[sv]);
         if (t + 1 < nt1) qk(t1, sk);
-        if (t + 1 < T) tc::mma_commit(&bars->op_empty[sk]);
+        if (t + 1 < T) commit(&bars->op_empty[sk]);
       }
       if (!ok) {  // no MMA outlives the allocation
-        tc::mma_commit(&bars->drained);
-        tc::mbar_sleep(&bars->drained, 0);
+        commit(&bars->drained);
+        wait(&bars->drained, 0);
       }
     }
   }

@@ -77,6 +77,19 @@ __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity,
   }
 }
 
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(one)
+      :
+      : "memory");
+  return one != 0;
+}
+
 // ---- TMA --------------------------------------------------------------------
 // 3D tiled load (no multicast) completing on `bar` with the byte count.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
