@@ -42,16 +42,17 @@
 #include "fc_kernels.h"
 #include "kv4.cuh"
 #include "kv4_attn.cuh"
+#include "kv4_ring.cuh"
 #include "tc_ptx.cuh"
 
 namespace fc {
 
 namespace {
-constexpr int kStep = 32;      // keys of a warp's step
-constexpr int kU = kStep / 16; // m16 tiles of a step
-constexpr int kGroup = 4;      // warps that work on one stage
-constexpr int kWarps = 8;      // two groups, taking stages in turn
-constexpr int kGroups = kWarps / kGroup;
+constexpr int kStep = kRingKeys;    // keys of a warp's step
+constexpr int kU = kStep / 16;      // m16 tiles of a step
+constexpr int kGroup = kRingWarps;  // warps that work on one stage
+constexpr int kGroups = kRingGroups;
+constexpr int kWarps = kGroups * kGroup;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStage = kGroup * kStep;
 static_assert(kStage == kStageKeys, "stages are the unit of the shares");
@@ -59,10 +60,7 @@ constexpr int kJoinWarps = 8;
 constexpr int kLeastStages = 2;  // of a block's share
 
 template <int D> constexpr int stage_bytes() { return kStage * (D + D / 8); }
-// A multiple of the groups, so that a stage's slot always belongs to one group: its
-// warps then wait for every phase of the slot's barrier, and a wait for one phase
-// cannot be answered by the phase two before it.
-template <int D> constexpr int stages() { return D == 128 ? 6 : 8; }
+template <int D> constexpr int stages() { return ring_slots(D); }
 // Outputs of a row at the end, with two numbers beside them and an odd stride.
 template <int D, int NR> constexpr int warp_result_bytes() { return NR * 8 * (D + 4) * 4; }
 template <int D, int NR> constexpr int ring_bytes() {
@@ -137,7 +135,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   constexpr int E = D / 4;          // elements of d that a thread holds of a key
   constexpr int CB = D / 2, SB = D / 16;
   constexpr int S = stages<D>();
-  static_assert(S % kGroups == 0, "a slot belongs to one group");
   constexpr int P = kF32 ? 2 : 1;   // float16 terms of queries and probabilities
   constexpr float kShift = kF32 ? 14.0f : 5.0f;
   constexpr float kSlack = kF32 ? 0.0f : 8.0f;
@@ -493,10 +490,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     __syncwarp();  // every lane has read the stage
     if (lane == 0) tc::mbar_arrive(&empty[s]);
   };
-  // One warp of the group, in turn, refills the stage that the group has released; it
-  // comes to that a softmax later than its own release, so the others have too.
   auto refill = [&](int i, int s, uint32_t parity) {
-    if (lane == 0 && i + S < n_stages && (i / kGroups) % kGroup == warp % kGroup) {
+    if (lane == 0 && ring_refills<S>(i, warp % kGroup, n_stages)) {
       if (tc::mbar_wait(&empty[s], parity))
         fetch(i + S, s);
       else
@@ -504,36 +499,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     }
   };
 
-  // Stages of the warp that hold keys for it, one ahead: the values of a stage and the
-  // logits of the next are independent work for one instruction stream.
-  const int n_mine = k_end - k_begin > w_off ? (k_end - k_begin - w_off + kStage - 1) / kStage : 0;
-  int i = (warp / kGroup + base) % kGroups;  // slots stay with their group
-  int slot = (base + i) % S;
-  uint32_t parity = ((base + i) / S) & 1;
-  if (i < n_mine && arrived(i, slot, parity)) {
-    logits(slot);
-    softmax(i, slot);
-    for (int nx = i + kGroups; nx < n_mine; nx += kGroups) {
-      int to = slot + kGroups;
-      uint32_t to_parity = parity;
-      if (to >= S) {
-        to -= S;
-        to_parity ^= 1;
-      }
-      if (!arrived(nx, to, to_parity)) break;
-      logits(to);
-      values(slot);
-      release(slot);
-      softmax(nx, to);
-      refill(i, slot, parity);
-      i = nx;
-      slot = to;
-      parity = to_parity;
-    }
-    if (ok) values(slot);
-  }
-  // every phase of a slot has its arrivals
-  for (; i < n_stages; i += kGroups) release((base + i) % S);
+  // Slots stay with their group of warps.  The waits of refill() are one lane's, so the
+  // lanes agree on whether a wait has given up before they go on together.
+  ring_walk<S>(base, (warp / kGroup + base) % kGroups,
+               ring_own_stages(k_end - k_begin, warp % kGroup), n_stages, arrived, logits, softmax,
+               values, release, refill, [&] { return __all_sync(0xffffffffu, ok) != 0; });
   if (!ok) atomicExch(a.err, 1);
   __syncthreads();
 

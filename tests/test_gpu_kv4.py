@@ -448,6 +448,34 @@ def test_attention_of_many_sequences(N, Hkv, dtype):
     _check(q[some], few, [int(lens[n]) for n in some], out[some], lse[some])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tail", [1, 33, 65, 96])
+def test_attention_short_last_stages(tail, d, dtype):
+    """Pieces of 7 to 20 stages of 128 keys whose last has keys for one to three of its four
+    warps, with a late maximum among one warp's keys: 256 units of the same numbers, ten
+    calls, all bitwise the same."""
+    g = torch.Generator().manual_seed(53 + tail)
+    N, H = 32, 8
+    for stages in (7, 8, 9, 13, 20):
+        keys = (stages - 1) * 128 + tail
+        cap = (keys + 15) // 16 * 16
+        k, v = _randn(g, 1, 1, cap, d), _randn(g, 1, 1, cap, d)
+        q = _randn(g, 1, 1, 1, d)
+        k[0, 0, keys - 128 + 40] = 3 * q[0, 0, 0]
+        one = fc.fc_kv4_cache(1, 1, cap, d)
+        fc.fc_kv4_store(k.to(DEV), v.to(DEV), one)
+        c = fc.Kv4Cache(*[t.expand(N, H, -1, -1).contiguous()
+                          for t in (one.k_codes, one.k_scales, one.v_codes, one.v_scales)])
+        q = q.to(dtype).to(DEV).expand(N, H, 1, d)
+        out, lse = _attend(q, c, keys)
+        assert _attend.launches == 1  # a block for each unit
+        _check(q[:1, :1], one, [keys], out[:1, :1], lse[:1, :1])
+        for _ in range(10):
+            assert torch.equal(out, out[:1, :1].expand_as(out)) and torch.equal(lse, lse[:1, :1].expand_as(lse))
+            out, lse = _attend(q, c, keys)
+
+
 def test_attention_refusals():
     c = fc.fc_kv4_cache(2, 2, 32, 64)
     q = torch.zeros(2, 4, 3, 64, device=DEV, dtype=BF16)
