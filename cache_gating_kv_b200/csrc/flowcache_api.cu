@@ -12,6 +12,7 @@
 #include "fc_common.cuh"
 #include "fc_kernels.h"
 #include "kv4.cuh"
+#include "tc_ptx.cuh"
 
 namespace fc {
 
@@ -36,6 +37,10 @@ void add_launches(int n) { g_launches += n; }
 namespace {
 
 thread_local char g_err[512] = "";
+
+// fc_selftest_kv4_stuck_slot
+thread_local int g_stuck_slot = -1;
+thread_local long long g_wait_cycles = fc::tc::kWaitCycles;
 
 fc_status fail(fc_status st, const char* fmt, ...) {
   va_list ap;
@@ -835,6 +840,8 @@ fc_status fc_kv4_attention(const void* q, const fc_kv4_cache* cache, const int32
   a.bf16 = dtype == FC_BF16;
   a.causal = causal != 0;
   a.scale = scale;
+  a.stuck_slot = g_stuck_slot;
+  a.wait_cycles = g_wait_cycles;
   return launched(fc::launch_kv4_attention(a, *cache, ws, static_cast<cudaStream_t>(stream)),
                   "fc_kv4_attention");
 }
@@ -857,6 +864,15 @@ fc_status fc_selftest_wait_timeout(long long limit_cycles, int* err, void* strea
   FC_CHECK_PTR(err);
   return launched(fc::launch_wait_selftest(limit_cycles, err, static_cast<cudaStream_t>(stream)),
                   "fc_selftest_wait_timeout");
+}
+
+fc_status fc_selftest_kv4_stuck_slot(int slot, long long limit_cycles) {
+  if (slot >= 0 && (limit_cycles < 0 || limit_cycles > fc::tc::kWaitCycles))
+    return fail(FC_ERR_INVALID_ARG, "limit_cycles must be in [0, 4e9]");
+  if (slot > 2) return fail(FC_ERR_INVALID_ARG, "slot must be at most 2 (got %d)", slot);
+  g_stuck_slot = slot < 0 ? -1 : slot;
+  g_wait_cycles = slot < 0 ? fc::tc::kWaitCycles : limit_cycles;
+  return ok();
 }
 
 }  // extern "C"

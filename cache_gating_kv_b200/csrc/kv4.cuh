@@ -117,6 +117,10 @@ struct Kv4Attn {
   int Hq, Lq, max_len;
   bool bf16, causal;
   float scale;  // of the logits, without 2^k_exp
+  // for the self-test of waits that give up: a slot of the ring of key stages whose
+  // barrier wants an arrival that nobody makes (-1: none)
+  int stuck_slot;
+  long long wait_cycles;
 };
 size_t kv4_attention_ws_bytes(bool bf16, int N, int Hq, int Hkv, int Lq, int max_len, int d);
 cudaError_t launch_kv4_attention(const Kv4Attn& a, const fc_kv4_cache& cache, void* ws,

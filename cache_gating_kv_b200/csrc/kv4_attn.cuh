@@ -26,6 +26,8 @@ struct AttnArgs {
   float scale_log2;  // scale * 2^k_exp * log2 e
   float out_scale;   // 2^v_exp
   int* err;
+  uint32_t wait_cycles;  // limit of a wait
+  int stuck_slot;         // of the ring: its barrier never completes (self-test; -1: none)
   // what blocks that share a unit leave for the join: by block (stream: two slots to a
   // block) and row
   float2* part_ml;  // [..][rows_blk] (log2 reference, sum)

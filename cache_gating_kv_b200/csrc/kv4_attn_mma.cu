@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&full[s], s == a.stuck_slot ? 2 : 1);
       tc::mbar_init(&empty[s], kGroup);
     }
     tc::fence_barrier_init();
@@ -478,11 +478,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
     }
   };
   auto arrived = [&](int i, int s, uint32_t parity) {
-    const bool in = __all_sync(0xffffffffu, tc::mbar_wait(&full[s], parity));
+    const bool in = __all_sync(0xffffffffu, tc::mbar_wait(&full[s], parity, a.wait_cycles));
     if (!in) {
       ok = false;
       for (int x = base + i; x < base + min(i + S, n_stages); ++x)  // copies under way
-        tc::mbar_wait(&full[x % S], (x / S) & 1, tc::kWaitCycles / 16);
+        tc::mbar_wait(&full[x % S], (x / S) & 1, tc::kDrainCycles);
     }
     return in;
   };
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
   };
   auto refill = [&](int i, int s, uint32_t parity) {
     if (lane == 0 && ring_refills<S>(i, warp % kGroup, n_stages)) {
-      if (tc::mbar_wait(&empty[s], parity))
+      if (tc::mbar_wait(&empty[s], parity, a.wait_cycles))
         fetch(i + S, s);
       else
         ok = false;
@@ -590,6 +590,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
   // (a share of equal work has no block for a unit without keys)
   int2 of = make_int2(0, 0);
   if (some || !a.stream) of = a.part_of[(int64_t)(n * a.Hkv + hk) * a.n_rb + rb];
+  // What a block that gave up a wait did not write is whatever the workspace held: no
+  // parts then (the error word is set), and no access by it.
+  const int leaving = a.blocks - a.n_whole;  // blocks that leave parts
+  if (of.x < 0 || of.x >= leaving || of.y < 1 || of.y > leaving - of.x) of = make_int2(0, 0);
   if (of.y == 1) return;  // one block had it all
   const int ns = of.y;
   // of equal shares: slot 1 of the first block, slot 0 of the others
@@ -811,6 +815,8 @@ cudaError_t launch_kv4_attention(const Kv4Attn& p, const fc_kv4_cache& c, void* 
   a.n_split = l.n_split;
   a.chunk = l.chunk;
   a.blocks = l.blocks;
+  a.stuck_slot = p.stuck_slot;
+  a.wait_cycles = (uint32_t)p.wait_cycles;
   char* w = static_cast<char*>(ws);
   a.err = reinterpret_cast<int*>(w);
   a.part_of = reinterpret_cast<int2*>(w + l.of);

@@ -11,6 +11,8 @@ namespace tc {
 
 // A bounded wait gives up after this many SM clocks (~2 s at 1.9 GHz).
 constexpr long long kWaitCycles = 4000000000ll;
+// What a thread that gave up leaves for its own copies in flight to land.
+constexpr long long kDrainCycles = kWaitCycles / 16;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -33,6 +33,17 @@ fc_status fc_selftest_exp2(const float* x, float* y_mufu, float* y_poly, int n, 
  */
 fc_status fc_selftest_wait_timeout(long long limit_cycles, int* err, void* stream);
 
+/*
+ * Failure-path self-test of fc_kv4_attention: in the calls that this host thread
+ * makes from now on, the barrier of slot `slot` of every block's ring of key stages
+ * wants one arrival more than is made, so that the waits for it run out, after
+ * `limit_cycles` SM clocks each; the call sets the workspace's error word (unless no
+ * block uses the slot) and returns normally.  A negative slot ends that (limit_cycles
+ * is then ignored).
+ * Errors: limit_cycles outside [0, 4e9], slot over 2 -> FC_ERR_INVALID_ARG.
+ */
+fc_status fc_selftest_kv4_stuck_slot(int slot, long long limit_cycles);
+
 #ifdef __cplusplus
 }
 #endif

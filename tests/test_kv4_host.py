@@ -140,3 +140,10 @@ def test_oracle_rotation_keeps_norms_and_relative_positions():
     assert max(dots) - min(dots) < 1e-10
     y = O.rope(q, [[[11]]], w)
     np.testing.assert_allclose(O.rope(y, [[[11]]], w, inverse=True), q, atol=1e-14)
+
+
+def test_stuck_slot_selftest_validates():
+    f = fc.library().fc_selftest_kv4_stuck_slot
+    f.restype, f.argtypes = ctypes.c_int, [ctypes.c_int, ctypes.c_longlong]
+    assert f(0, -1) == 1 and f(0, 4_000_000_001) == 1 and f(3, 0) == 1
+    assert f(2, 1000) == 0 and f(-1, 0) == 0
