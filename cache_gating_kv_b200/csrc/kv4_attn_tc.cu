@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCodes; ++i) {
-      tc::mbar_init(&bars->code_full[i], 1);
+      tc::mbar_init(&bars->code_full[i], i == a.stuck_slot ? 2 : 1);
       tc::mbar_init(&bars->code_empty[i], 4);
     }
     for (int i = 0; i < kOps; ++i) {
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     float ref = -INFINITY;
     float2 l2 = make_float2(0.f, 0.f);
     for (int t = 0; t < nt[j]; ++t) {
-      if (!__all_sync(0xffffffffu, tc::mbar_sleep(&bars->s_full[j], t & 1))) {
+      if (!__all_sync(0xffffffffu, tc::mbar_sleep(&bars->s_full[j], t & 1, a.wait_cycles))) {
         ok = false;
         break;
       }
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     }
     // ---- the row's result
     if (ok && nt[j] > 0) {
-      ok = __all_sync(0xffffffffu, tc::mbar_sleep(&bars->o_full[j], 0));
+      ok = __all_sync(0xffffffffu, tc::mbar_sleep(&bars->o_full[j], 0, a.wait_cycles));
       tc::fence_after_sync();
     }
     if (!idle) {
@@ -341,11 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     const int turn = (part >> 1) * 2;
     for (int h = 0; h < 2 * T; ++h) {
       const int cs = h % kCodes, os = h % kOps;
-      if (!tc::mbar_sleep(&bars->code_full[cs], (h / kCodes) & 1) ||
-          !tc::mbar_sleep(&bars->op_empty[os], ((h / kOps) & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
+      // the lanes go on together or not at all: a warp split between its own barrier and
+      // the block's might wait for ever
+      ok = __all_sync(0xffffffffu,
+                      tc::mbar_sleep(&bars->code_full[cs], (h / kCodes) & 1, a.wait_cycles) &&
+                          tc::mbar_sleep(&bars->op_empty[os], ((h / kOps) & 1) ^ 1, a.wait_cycles));
+      if (!ok) break;
       const bool key = (h & 1) == 0;
       const uint8_t* codes = sCode + cs * kCode;
       const uint8_t* scales = codes + kN * CB;
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       int h = 0;
       for (; h < 2 * T; ++h) {
         const int cs = h % kCodes;
-        if (!tc::mbar_sleep(&bars->code_empty[cs], ((h / kCodes) & 1) ^ 1)) {
+        if (!tc::mbar_sleep(&bars->code_empty[cs], ((h / kCodes) & 1) ^ 1, a.wait_cycles)) {
           ok = false;
           break;
         }
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
         }
       }
       for (int x = max(0, h - kCodes); x < h; ++x)  // no copy outlives the block
-        ok &= tc::mbar_sleep(&bars->code_full[x % kCodes], (x / kCodes) & 1);
+        ok &= tc::mbar_sleep(&bars->code_full[x % kCodes], (x / kCodes) & 1, tc::kDrainCycles);
     } else if (warp == 13 && T > 0) {
       // ---- MMA issue.  The logits of a tile wait for this warp twice a step, so it
       // keeps no arrays and finds its descriptors by additions.  The warp stays together
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       const uint64_t k_desc = tc::desc_k_sw128(tc::smem_u32(sOp));
       const uint64_t v_desc = tc::desc_mn_sw128(tc::smem_u32(sOp), kN * 128);
       auto wait = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, tc::mbar_sleep(bar, phase & 1)) != 0;
+        return __all_sync(0xffffffffu, tc::mbar_sleep(bar, phase & 1, a.wait_cycles)) != 0;
       };
       auto qk = [&](auto jc, int os) {
         constexpr int j = decltype(jc)::value;
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
       }
       if (!ok) {  // no MMA outlives the allocation
         commit(&bars->drained);
-        wait(&bars->drained, 0);
+        tc::mbar_sleep(&bars->drained, 0);
       }
     }
   }

@@ -36,10 +36,12 @@ def _random_cache(N, H, cap, d):
 
 
 # A unit that several blocks share; shares that hold several units; a block for each unit,
-# with stages behind the ring; the same of float32 and 16 rows.  `most`: the slots that a block uses at most.  The first case
+# with stages behind the ring; the same of float32 and 16 rows; many rows, whole units and
+# units split along the keys.  `most`: the slots that a block uses at most.  The first case
 # has 4 x (47 + 3 + 40 + 3) = 372 of work for 148 x 2 blocks, which get two stages at least.
 CASES = [(BF16, 2, 4, 4, 1, 128, [6000, 5000], 2, 2), (BF16, 100, 2, 2, 1, 64, [4400, 130] * 50, 2, 8),
-         (BF16, 8, 32, 32, 1, 128, [1100] * 8, 1, 6), (F32, 20, 8, 4, 8, 64, [1400] * 20, 1, 8)]
+         (BF16, 8, 32, 32, 1, 128, [1100] * 8, 1, 6), (F32, 20, 8, 4, 8, 64, [1400] * 20, 1, 8),
+         (BF16, 2, 2, 2, 200, 128, [500, 470], 1, 3), (BF16, 1, 2, 2, 300, 64, [6000], 2, 3)]
 
 
 @pytest.mark.parametrize("slot", [0, 1, 2])
