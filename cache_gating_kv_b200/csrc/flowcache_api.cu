@@ -223,6 +223,12 @@ fc_status check_plan(const fc_rope_plan* p) {
   return FC_OK;
 }
 
+// Two arguments that are both given and share memory.  (Addresses only: these checks come
+// before the queries of the pointers, so NULL is still possible.)
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  return a != nullptr && b != nullptr && ranges_overlap(a, na, b, nb);
+}
+
 struct CacheSpans {
   size_t codes, scales;
 };
@@ -238,19 +244,32 @@ fc_status check_cache(const fc_kv4_cache* c, CacheSpans* out) {
                 c->cap);
   if (c->k_exp < -64 || c->k_exp > 64 || c->v_exp < -64 || c->v_exp > 64)
     return fail(FC_ERR_INVALID_ARG, "cache: k_exp and v_exp must be in [-64, 64]");
-  FC_TRY(check_ptr_here(c->k_codes, "cache k_codes"));
-  FC_TRY(check_ptr_here(c->k_scales, "cache k_scales"));
-  FC_TRY(check_ptr_here(c->v_codes, "cache v_codes"));
-  FC_TRY(check_ptr_here(c->v_scales, "cache v_scales"));
   const size_t rows = (size_t)c->N * c->H * c->cap;
   out->codes = rows * (c->d / 2);
   out->scales = rows * (c->d / 16);
   return FC_OK;
 }
 
+// A cache that is written: its four buffers are apart.
+fc_status check_cache_apart(const fc_kv4_cache* c, const CacheSpans& s) {
+  const void* p[4] = {c->k_codes, c->v_codes, c->k_scales, c->v_scales};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(p[i], i < 2 ? s.codes : s.scales, p[j], j < 2 ? s.codes : s.scales))
+        return fail(FC_ERR_INVALID_ARG, "cache: its codes and scales overlap one another");
+  return FC_OK;
+}
+
+fc_status check_cache_ptrs(const fc_kv4_cache* c) {
+  FC_TRY(check_ptr_here(c->k_codes, "cache k_codes"));
+  FC_TRY(check_ptr_here(c->k_scales, "cache k_scales"));
+  FC_TRY(check_ptr_here(c->v_codes, "cache v_codes"));
+  return check_ptr_here(c->v_scales, "cache v_scales");
+}
+
 bool overlaps_cache(const fc_kv4_cache* c, const CacheSpans& s, const void* p, size_t n) {
-  return ranges_overlap(c->k_codes, s.codes, p, n) || ranges_overlap(c->v_codes, s.codes, p, n) ||
-         ranges_overlap(c->k_scales, s.scales, p, n) || ranges_overlap(c->v_scales, s.scales, p, n);
+  return overlap(c->k_codes, s.codes, p, n) || overlap(c->v_codes, s.codes, p, n) ||
+         overlap(c->k_scales, s.scales, p, n) || overlap(c->v_scales, s.scales, p, n);
 }
 
 }  // namespace
@@ -734,17 +753,23 @@ fc_status fc_kv4_store(const void* k, const void* v, fc_dtype dtype, int N, int 
       return fail(FC_ERR_INVALID_ARG, "rot_dim %d is over d %d", rope->rot_dim, d);
     if (idx != nullptr)
       return fail(FC_ERR_UNSUPPORTED, "rope with idx: a selection reads rows that are rotated already");
-    FC_TRY(check_ptr_here(pos, "pos"));
   }
   View vk, vv;
   FC_TRY(check_view(k_strides, dtype, N, H, L, d, false, "k", &vk));
   FC_TRY(check_view(v_strides, dtype, N, H, L, d, false, "v", &vv));
+  FC_TRY(check_cache_apart(cache, cs));
+  if (overlaps_cache(cache, cs, k, vk.span) || overlaps_cache(cache, cs, v, vv.span))
+    return fail(FC_ERR_INVALID_ARG, "k or v overlaps the cache");
+  if (overlaps_cache(cache, cs, idx, (size_t)N * H * B * 4) ||
+      overlaps_cache(cache, cs, row0_dev, (size_t)N * 4) ||
+      (rope != nullptr && overlaps_cache(cache, cs, pos, (size_t)rope->n_axes * N * L * 4)))
+    return fail(FC_ERR_INVALID_ARG, "idx, row0_dev or pos overlaps the cache");
+  FC_TRY(check_cache_ptrs(cache));
   FC_TRY(check_ptr_here(k, "k"));
   FC_TRY(check_ptr_here(v, "v"));
   if (idx != nullptr) FC_TRY(check_ptr_here(idx, "idx"));
   if (row0_dev != nullptr) FC_TRY(check_ptr_here(row0_dev, "row0_dev"));
-  if (overlaps_cache(cache, cs, k, vk.span) || overlaps_cache(cache, cs, v, vv.span))
-    return fail(FC_ERR_INVALID_ARG, "k or v overlaps the cache");
+  if (rope != nullptr) FC_TRY(check_ptr_here(pos, "pos"));
   return launched(fc::launch_kv4_store(k, v, dtype == FC_BF16, L, vk.st, vv.st, idx,
                                        idx != nullptr ? B : L, row0, row0_dev, rope, pos, *cache,
                                        static_cast<cudaStream_t>(stream)),
@@ -764,12 +789,16 @@ fc_status fc_kv4_load(const fc_kv4_cache* cache, void* k_out, void* v_out, fc_dt
   View vk, vv;
   FC_TRY(check_view(k_strides, dtype, cache->N, cache->H, L, cache->d, true, "k_out", &vk));
   FC_TRY(check_view(v_strides, dtype, cache->N, cache->H, L, cache->d, true, "v_out", &vv));
+  if (overlaps_cache(cache, cs, k_out, vk.span) || overlaps_cache(cache, cs, v_out, vv.span) ||
+      overlap(k_out, vk.span, v_out, vv.span))
+    return fail(FC_ERR_INVALID_ARG, "k_out / v_out overlap the cache or each other");
+  const size_t row0_bytes = (size_t)cache->N * 4;
+  if (overlap(row0_dev, row0_bytes, k_out, vk.span) || overlap(row0_dev, row0_bytes, v_out, vv.span))
+    return fail(FC_ERR_INVALID_ARG, "row0_dev overlaps k_out or v_out");
+  FC_TRY(check_cache_ptrs(cache));
   FC_TRY(check_ptr_here(k_out, "k_out"));
   FC_TRY(check_ptr_here(v_out, "v_out"));
   if (row0_dev != nullptr) FC_TRY(check_ptr_here(row0_dev, "row0_dev"));
-  if (overlaps_cache(cache, cs, k_out, vk.span) || overlaps_cache(cache, cs, v_out, vv.span) ||
-      ranges_overlap(k_out, vk.span, v_out, vv.span))
-    return fail(FC_ERR_INVALID_ARG, "k_out / v_out overlap the cache or each other");
   return launched(fc::launch_kv4_load(*cache, k_out, v_out, dtype == FC_BF16, L, vk.st, vv.st, row0,
                                       row0_dev, static_cast<cudaStream_t>(stream)),
                   "fc_kv4_load");
@@ -809,23 +838,23 @@ fc_status fc_kv4_attention(const void* q, const fc_kv4_cache* cache, const int32
   View vq, vo;
   FC_TRY(check_view(q_strides, dtype, N, Hq, Lq, d, false, "q", &vq));
   FC_TRY(check_view(out_strides, dtype, N, Hq, Lq, d, true, "out", &vo));
+  const size_t lse_bytes = (size_t)N * Hq * Lq * sizeof(float), lens_bytes = (size_t)N * 4;
+  if (overlap(lse, lse_bytes, q, vq.span) || overlap(lse, lse_bytes, out, vo.span) ||
+      overlap(lse, lse_bytes, ws, need) || overlap(lse, lse_bytes, lens, lens_bytes) ||
+      overlaps_cache(cache, cs, lse, lse_bytes))
+    return fail(FC_ERR_INVALID_ARG, "lse overlaps another argument");
+  if (overlap(out, vo.span, q, vq.span) || overlap(out, vo.span, ws, need) ||
+      overlap(out, vo.span, lens, lens_bytes) || overlaps_cache(cache, cs, out, vo.span))
+    return fail(FC_ERR_INVALID_ARG, "out overlaps another argument");
+  if (overlap(ws, need, q, vq.span) || overlap(ws, need, lens, lens_bytes) ||
+      overlaps_cache(cache, cs, ws, need))
+    return fail(FC_ERR_INVALID_ARG, "ws overlaps another argument");
+  FC_TRY(check_cache_ptrs(cache));
   FC_TRY(check_ptr_here(q, "q"));
   FC_TRY(check_ptr_here(out, "out"));
   FC_TRY(check_ptr_here(ws, "ws"));
   if (lens != nullptr) FC_TRY(check_ptr_here(lens, "lens"));
-  const size_t lse_bytes = (size_t)N * Hq * Lq * sizeof(float);
-  if (lse != nullptr) {
-    FC_TRY(check_ptr_here(lse, "lse"));
-    if (ranges_overlap(lse, lse_bytes, q, vq.span) || ranges_overlap(lse, lse_bytes, out, vo.span) ||
-        ranges_overlap(lse, lse_bytes, ws, need) || overlaps_cache(cache, cs, lse, lse_bytes))
-      return fail(FC_ERR_INVALID_ARG, "lse overlaps another argument");
-  }
-  if (ranges_overlap(out, vo.span, q, vq.span) || ranges_overlap(out, vo.span, ws, need) ||
-      overlaps_cache(cache, cs, out, vo.span) ||
-      (lens != nullptr && ranges_overlap(lens, (size_t)N * 4, out, vo.span)))
-    return fail(FC_ERR_INVALID_ARG, "out overlaps another argument");
-  if (ranges_overlap(ws, need, q, vq.span) || overlaps_cache(cache, cs, ws, need))
-    return fail(FC_ERR_INVALID_ARG, "ws overlaps another argument");
+  if (lse != nullptr) FC_TRY(check_ptr_here(lse, "lse"));
   if (!(scale > 0.0f)) scale = 1.0f / sqrtf((float)d);
   fc::Kv4Attn a = {};
   a.q = q;

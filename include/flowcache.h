@@ -525,7 +525,8 @@ typedef struct {
  *            rotated first, in float32, without another rounding.  Not together
  *            with idx (a selection reads rows that are rotated already).
  * Rows of the cache outside [row0, row0 + rows) are left as they were; rows
- * that would fall outside [0, cap) are not written.  k and v must not overlap the cache.
+ * that would fall outside [0, cap) are not written.  k, v, idx, row0_dev and pos must
+ * not overlap the cache, whose four buffers must not overlap one another.
  * Errors: bad sizes, strides or pointers -> FC_ERR_INVALID_ARG; d not 64 or
  * 128, or rope with idx -> FC_ERR_UNSUPPORTED.
  */
@@ -539,6 +540,7 @@ fc_status fc_kv4_store(const void* k, const void* v, fc_dtype dtype, int N, int 
  * (fc_kv_importance, fc_kv_redundancy, fc_kv_compact): exact in both dtypes.
  *   k_out, v_out  [N][H][L][d] dtype with strides
  *   row0, row0_dev  as for fc_kv4_store; rows outside [0, cap) give zeros
+ * k_out, v_out, row0_dev and the cache must not overlap one another.
  * Errors as for fc_kv4_store.
  */
 fc_status fc_kv4_load(const fc_kv4_cache* cache, void* k_out, void* v_out, fc_dtype dtype, int L,
@@ -558,7 +560,8 @@ size_t fc_kv4_attention_workspace_size(fc_dtype dtype, int N, int Hq, int Hkv, i
  * queries are the last Lq positions of the sequence).  A query that sees no key
  * has out = 0 and lse = -inf.
  *
- *   q, out   [N][Hq][Lq][d] dtype with strides; out must not overlap q
+ *   q, out   [N][Hq][Lq][d] dtype with strides; out, lse and ws must not overlap one
+ *            another or anything that is read
  *   cache    N and d as q; Hq a multiple of its H
  *   lens     [N] int32 (device), or NULL: every sequence has max_len keys.
  *            Values outside [0, max_len] are clamped.

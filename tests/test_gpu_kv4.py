@@ -609,3 +609,17 @@ def test_compression_into_the_cache_together():
         assert torch.equal(nxt.v_scales[0, h, :B], c.v_scales[0, h, i])
     out, lse = _attend(q[None], nxt, B)
     _check(q[None], nxt, [B], out, lse)
+
+
+def test_keys_that_are_the_values():
+    """A cache may be read with one set of buffers for keys and values; writing it is refused."""
+    g = torch.Generator().manual_seed(97)
+    c = _cache(g, 1, 2, 80, 64)
+    same = fc.Kv4Cache(c.k_codes, c.k_scales, c.k_codes, c.k_scales)
+    for Lq in (1, 130):
+        q = _randn(g, 1, 4, Lq, 64).to(BF16).to(DEV)
+        out, lse = _attend(q, same, 77)
+        _check(q, same, [77], out, lse)
+    x = torch.zeros(1, 2, 3, 64, device=DEV)
+    with pytest.raises(fc.FlowCacheError, match="overlap"):
+        fc.fc_kv4_store(x, x, same)

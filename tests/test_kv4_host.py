@@ -147,3 +147,61 @@ def test_stuck_slot_selftest_validates():
     f.restype, f.argtypes = ctypes.c_int, [ctypes.c_int, ctypes.c_longlong]
     assert f(0, -1) == 1 and f(0, 4_000_000_001) == 1 and f(3, 0) == 1
     assert f(2, 1000) == 0 and f(-1, 0) == 0
+
+
+def _fake(n):
+    """An aligned address per n; overlap is refused before a pointer is asked about."""
+    return 0x7F00_0000_0000 + n * (1 << 24)
+
+
+def _refused(status):
+    return status == 1 and b"overlap" in fc.library().fc_last_error()
+
+
+def test_buffers_of_a_cache_that_is_written_must_be_apart():
+    lib, r = fc.library(), ctypes.byref
+    size = {0: 16 * 32, 1: 16 * 4, 2: 16 * 32, 3: 16 * 4}  # k codes, k scales, v codes, v scales
+    for i in range(4):
+        for j in range(4):
+            if i == j:
+                continue
+            at = [_fake(n) for n in range(4)]
+            at[j] = at[i] + size[i] - 16  # the last 16 bytes
+            c = fc._Kv4(*at, 1, 1, 16, 64, 0, 0)
+            store = lambda: lib.fc_kv4_store(_fake(8), _fake(9), 1, 1, 1, 4, 64, None, None, None, 0, 0, None,  # noqa: E731
+                                             None, None, r(c), None)
+            assert _refused(store())
+            # who only reads may share them (keys that are the values)
+            assert not _refused(lib.fc_kv4_load(r(c), _fake(8), _fake(9), 1, 4, None, None, 0, None, None))
+            assert not _refused(lib.fc_kv4_attention(_fake(8), r(c), None, 16, 1, 1, 1, 1, 64, None, 0, 0.0, _fake(9),
+                                                     None, None, _fake(10), 1 << 20, None))
+            at[j] = at[i] + size[i]  # behind it; the addresses are nobody's
+            c = fc._Kv4(*at, 1, 1, 16, 64, 0, 0)
+            assert not _refused(store()) and b"overlap" not in fc.library().fc_last_error()
+
+
+def test_arrays_that_are_read_must_be_apart_from_what_is_written():
+    lib, r = fc.library(), ctypes.byref
+    c = fc._Kv4(*[_fake(n) for n in range(4)], 2, 2, 16, 64, 0, 0)
+    size = [64 * 32, 64 * 4, 64 * 32, 64 * 4]
+    p = fc.fc_rope_init(64, sections=[16, 16])
+    for n in range(4):
+        end = _fake(n) + size[n] - 16
+        store = lambda **a: lib.fc_kv4_store(  # noqa: E731
+            _fake(8), _fake(9), 1, 2, 2, 4, 64, None, None, a.get("idx"), 3 if "idx" in a else 0, 0, a.get("row0"),
+            r(p) if "pos" in a else None, a.get("pos"), r(c), None)
+        for name, nbytes in (("idx", 2 * 2 * 3 * 4), ("row0", 8), ("pos", 2 * 2 * 4 * 4)):
+            assert _refused(store(**{name: end})), name
+            assert nbytes <= 16 or _refused(store(**{name: _fake(n) - 16})), name  # its end in the buffer
+            store(**{name: end + 16})
+            assert b"overlap" not in lib.fc_last_error()
+    for out in (8, 9):
+        assert _refused(lib.fc_kv4_load(r(c), _fake(8), _fake(9), 1, 4, None, None, 0, _fake(out) + 16, None))
+    attend = lambda lens=_fake(11), lse=_fake(12): lib.fc_kv4_attention(  # noqa: E731
+        _fake(8), r(c), lens, 16, 1, 2, 2, 1, 64, None, 0, 0.0, _fake(9), None, lse, _fake(10), 1 << 20, None)
+    assert not _refused(attend())
+    assert _refused(attend(lens=_fake(9)))
+    assert _refused(attend(lens=_fake(12)))
+    assert _refused(attend(lens=_fake(10) + 16))
+    assert _refused(attend(lse=_fake(8))) and _refused(attend(lse=_fake(9))) and _refused(attend(lse=_fake(10)))
+    assert _refused(attend(lse=_fake(3)))
