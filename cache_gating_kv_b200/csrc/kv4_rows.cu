@@ -212,16 +212,18 @@ __global__ void __launch_bounds__(kThreads, 4)
     for (int k = 0; k < kUnroll; ++k, o += o_step) {
       if (!put[k]) continue;
       float y[16];
+      const bool turn = rotate && g * 16 < plan.rot_dim && from[k] != nullptr;
 #pragma unroll
       for (int i = 0; i < kRaw; ++i) {
-        const uint32_t flip = sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
-        raw[k][i].x ^= flip;  // (rotation and maximum do not mind)
+        // to the negatives: of what is rotated only behind it, since a zero that a
+        // rotation of negatives gives has not the sign of the zero that it stands for
+        const uint32_t flip = turn ? 0u : sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
+        raw[k][i].x ^= flip;
         raw[k][i].y ^= flip;
         raw[k][i].z ^= flip;
         raw[k][i].w ^= flip;
         Vec16<T>::to_float(raw[k][i], y + i * (16 / kRaw));
       }
-      const bool turn = rotate && g * 16 < plan.rot_dim && from[k] != nullptr;
       if (turn) {
         const float2* c = cs + (threadIdx.x / G & (a.T - 1)) * half;  // (by heads)
         if constexpr (kRope == 1) {
@@ -230,8 +232,6 @@ __global__ void __launch_bounds__(kThreads, 4)
             float z[16];
             const bool low = g * 16 < half;
             load16(from[k] + (low ? half : -half), z);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = -z[i];
             c += low ? g * 16 : g * 16 - half;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -241,9 +241,9 @@ __global__ void __launch_bounds__(kThreads, 4)
             for (int i = 0; i < 16; ++i) {
               const int e = g * 16 + i;
               if (e < half)
-                y[i] = rope_a(y[i], -load1(row + e + half), c[e]);
+                y[i] = rope_a(y[i], load1(row + e + half), c[e]);
               else if (e < plan.rot_dim)
-                y[i] = rope_b(-load1(row + e - half), y[i], c[e - half]);
+                y[i] = rope_b(load1(row + e - half), y[i], c[e - half]);
             }
           }
         } else if constexpr (kRope == 2) {
@@ -257,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, 4)
             }
           }
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = -y[i];
       }
       float amax;
       if constexpr (sizeof(T) == 2)

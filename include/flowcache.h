@@ -511,7 +511,8 @@ typedef struct {
  *   scale = e4m3(min(a / 6, 448)),  code = e2m1(y / scale),
  * both divisions rounded to float32, both conversions to nearest with ties to
  * even, the second one saturating at 6 (so an infinity is stored as the largest
- * number, 6 * 448).  A scale of zero has zero codes.  A group with a NaN gets a
+ * number, 6 * 448).  Codes keep the number's sign,
+ * also of a zero; a scale of zero has zeros for codes.  A group with a NaN gets a
  * NaN scale.  Storing what fc_kv4_load returned gives the same bits again while
  * the scales are normal (>= 2^-6).
  *

@@ -623,3 +623,35 @@ def test_keys_that_are_the_values():
     x = torch.zeros(1, 2, 3, 64, device=DEV)
     with pytest.raises(fc.FlowCacheError, match="overlap"):
         fc.fc_kv4_store(x, x, same)
+
+
+# ---- signs of zeros ---------------------------------------------------------------
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(128, 128), (64, 32), (64, 24), (64, 6)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_store_rotates_zeros_as_fc_rope(dtype, d, rot, interleaved):
+    """Zeros of both signs, pairs that cancel, whole rows of zeros (a padded row): the bits
+    of fc_rope in float32 and a plain store, signs of zeros among them."""
+    g = torch.Generator().manual_seed(13)
+    N, H, L = 2, 3, 24
+    k = _randn(g, N, H, L, d).to(dtype)
+    k[:, :, 0] = 0.0
+    k[:, :, 1] = -0.0
+    k[:, :, 2, ::2], k[:, :, 2, 1::2] = 0.0, -0.0
+    k[:, :, 3, : rot // 2], k[:, :, 3, rot // 2: rot] = 0.0, -0.0
+    k[torch.rand(N, H, L, d, generator=g) < 0.3] = 0.0
+    k[torch.rand(N, H, L, d, generator=g) < 0.2] = -0.0
+    k = k.to(DEV)
+    plan = fc.fc_rope_init(rot, int(interleaved))
+    pos = torch.randint(-50, 50, (N, L), generator=g).to(torch.int32)
+    pos[:, 4:8] = 0  # no turn: cos 1, sin 0
+    pos = pos.to(DEV)
+    a, b = fc.fc_kv4_cache(N, H, 32, d), fc.fc_kv4_cache(N, H, 32, d)
+    fc.fc_kv4_store(k, k, a, rope=plan, pos=pos)
+    k32 = torch.empty(N, H, L, d, device=DEV)
+    fc.fc_rope(k.float(), k32, pos, plan)
+    fc.fc_kv4_store(k32, k.float(), b)
+    for n in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
+    code, sc = O.kv4_quantise(k32.cpu().numpy())
+    assert np.array_equal(_bytes(b.k_codes)[:, :, :L], O.kv4_pack(code))
