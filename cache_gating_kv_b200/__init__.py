@@ -487,9 +487,9 @@ def fc_kv4_attention_workspace_size(dtype, N, Hq, Hkv, Lq, max_len, d):
 def fc_kv4_attention(q, cache, lens, out, ws, max_len=None, causal=False, scale=0.0, lse=None,
                      stream=None):
     """Attention of q [N, Hq, Lq, d] (or [Hq, Lq, d]) over the cache.  lens: [N] int32
-    on the device, an int for all sequences, or None (max_len of each); max_len
-    bounds the lengths (cap if None).  out like q; lse [N, Hq, Lq] float32 or None;
-    ws from :func:`fc_kv4_attention_workspace_size`."""
+    on the device, an int (at most max_len) for all sequences, or None (max_len of
+    each); max_len bounds the lengths (cap if None; those on the device are clamped).
+    out like q; lse [N, Hq, Lq] float32 or None; ws from :func:`fc_kv4_attention_workspace_size`."""
     qp, (N, Hq, Lq, d), qs = _rows(q, "q")
     op, oshape, os_ = _rows(out, "out")
     if oshape != (N, Hq, Lq, d) or out.dtype != q.dtype:
@@ -500,7 +500,9 @@ def fc_kv4_attention(q, cache, lens, out, ws, max_len=None, causal=False, scale=
     if isinstance(lens, torch.Tensor):
         lp = _ints(lens, N, "lens")
     elif lens is not None:
-        max_len = min(int(lens), int(max_len))
+        if int(lens) > int(max_len):
+            raise FlowCacheError(f"FC_ERR_INVALID_ARG: lens {int(lens)} is over max_len {int(max_len)}", 1)
+        max_len = int(lens)
     if lse is not None and (lse.dtype != torch.float32 or lse.numel() != N * Hq * Lq):
         raise FlowCacheError("lse must be [N, Hq, Lq] float32")
     st = library().fc_kv4_attention(qp, cache._ref, lp, int(max_len), _dtype_code(q),

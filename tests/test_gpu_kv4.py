@@ -625,6 +625,17 @@ def test_keys_that_are_the_values():
         fc.fc_kv4_store(x, x, same)
 
 
+def test_attention_host_length_over_the_limit_is_refused():
+    c = fc.fc_kv4_cache(2, 2, 32, 64)
+    q = torch.zeros(2, 4, 3, 64, device=DEV, dtype=BF16)
+    o, ws = torch.empty_like(q), fc.workspace(1 << 16)
+    fc.fc_kv4_attention(q, c, 32, o, ws)
+    fc.fc_kv4_attention(q, c, 20, o, ws, max_len=20)
+    for lens, max_len in ((33, None), (21, 20), (33, 40)):
+        with pytest.raises(fc.FlowCacheError, match="INVALID_ARG"):
+            fc.fc_kv4_attention(q, c, lens, o, ws, max_len=max_len)
+
+
 # ---- signs of zeros ---------------------------------------------------------------
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("d,rot", [(128, 128), (64, 32), (64, 24), (64, 6)])
