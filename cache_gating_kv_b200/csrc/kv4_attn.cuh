@@ -223,11 +223,15 @@ template <typename T>
 __device__ __forceinline__ void write_row(const AttnArgs& a, int n, int hk, int r, int c, float4 o,
                                           float ref, float L) {
   const int i = r / a.G, h = hk * a.G + r % a.G;
-  const float f = L == 0.0f ? 0.0f : __fdividef(a.out_scale, L);
   T* p = static_cast<T*>(a.out) + n * a.os.n + h * a.os.h + i * a.os.l + c;
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  if constexpr (sizeof(T) == 4) {  // each quotient rounds once
+    const float by = L == 0.0f ? 1.0f : L, up = L == 0.0f ? 0.0f : a.out_scale;
+    *reinterpret_cast<float4*>(p) = make_float4(__fdiv_rn(o.x, by) * up, __fdiv_rn(o.y, by) * up,
+                                                __fdiv_rn(o.z, by) * up, __fdiv_rn(o.w, by) * up);
   } else {
+    // 2 ulps of float32 here, in front of a rounding to 8 bits (L is far below the 2^126
+    // from which this quotient would be zero)
+    const float f = L == 0.0f ? 0.0f : __fdividef(a.out_scale, L);
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * f, o.y * f);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * f, o.w * f);
     *reinterpret_cast<uint2*>(p) = make_uint2(reinterpret_cast<const uint32_t&>(lo),

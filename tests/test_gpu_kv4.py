@@ -476,6 +476,23 @@ def test_attention_short_last_stages(tail, d, dtype):
             out, lse = _attend(q, c, keys)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("keys", [49, 1000, 2900])
+def test_attention_f32_divides_exactly(keys, d):
+    """Equal keys and equal values, float32: every probability is the same power of two, so
+    numerator (n v 2^k, v of six bits) and denominator are exact and so is the quotient."""
+    g = torch.Generator().manual_seed(keys)
+    for n in range(keys - 8, keys + 1):
+        c = fc.fc_kv4_cache(1, 2, 2912, d, v_exp=3)
+        v = _randn(g, 1, 2, 1, d).to(DEV).expand(1, 2, n, d)
+        fc.fc_kv4_store(torch.zeros(1, 2, n, d, device=DEV), v, c)
+        got = [torch.empty(1, 2, n, d, device=DEV) for _ in range(2)]
+        fc.fc_kv4_load(c, *got)
+        q = _randn(g, 1, 4, 3, d).to(DEV)
+        out, _ = _attend(q, c, n, max_len=n)
+        assert torch.equal(out, got[1][:, :, :1].repeat_interleave(2, 1).expand_as(out)), n
+
+
 def test_attention_refusals():
     c = fc.fc_kv4_cache(2, 2, 32, 64)
     q = torch.zeros(2, 4, 3, 64, device=DEV, dtype=BF16)
