@@ -90,9 +90,10 @@ fc_status check_ptr(const void* p, const char* name, int dev = -1) {
   } while (0)
 
 fc_status launched(cudaError_t e, const char* what) {
-  if (e != cudaSuccess) fc::g_launches = 0;
-  if (e != cudaSuccess) return fail(FC_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
-  return ok();
+  if (e == cudaSuccess) return ok();
+  fc::g_launches = 0;
+  cudaGetLastError();  // reported here: the next call's launch starts without it
+  return fail(FC_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
 }
 
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -432,7 +433,10 @@ fc_status fc_check_workspace(fc_ws_kind kind, const void* ws, int n_chunks, int 
                     fc::gate_noalloc_max_chunks());
       void* p = nullptr;
       const cudaError_t e = fc::gate_noalloc_scratch(&p);
-      if (e != cudaSuccess) return fail(FC_ERR_CUDA, "scratch address: %s", cudaGetErrorString(e));
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(FC_ERR_CUDA, "scratch address: %s", cudaGetErrorString(e));
+      }
       base = static_cast<const char*>(p);
       off = (size_t)n_chunks * sizeof(unsigned);
       break;
@@ -452,7 +456,10 @@ fc_status fc_check_workspace(fc_ws_kind kind, const void* ws, int n_chunks, int 
     e = cudaMemsetAsync(const_cast<char*>(base) + off, 0, sizeof(int), s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   }
-  if (e != cudaSuccess) return fail(FC_ERR_CUDA, "reading the error word: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(FC_ERR_CUDA, "reading the error word: %s", cudaGetErrorString(e));
+  }
   if (word != 0)
     return fail(FC_ERR_TIMEOUT, "a bounded device-side wait gave up: the outputs of the "
                                 "calls since the word was last clear are not valid");

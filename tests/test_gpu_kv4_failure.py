@@ -78,3 +78,31 @@ def test_slot_that_no_block_reaches_is_not_missed(stick):
     stick(2)
     fc.fc_kv4_attention(q, c, None, out, ws)
     assert fc.fc_check_workspace(fc.FC_WS_IMPORTANCE, ws) and torch.equal(out, want)
+
+
+def test_refused_launch_leaves_no_error_behind():
+    """A launch that the driver refuses (into a capture that is broken already) is reported by
+    its own call and not again by the next one, which is in order."""
+    cu = ctypes.CDLL("libcuda.so.1")
+    vp = ctypes.c_void_p
+    x = torch.randn(1, 2, 8, 64, device=DEV)
+    pos = torch.arange(8, dtype=torch.int32, device=DEV)
+    plan = fc.fc_rope_init(64)
+    want, y = torch.empty_like(x), torch.empty_like(x)
+    fc.fc_rope(x, want, pos, plan)
+    torch.cuda.synchronize()
+    s = vp()
+    assert cu.cuStreamCreate(ctypes.byref(s), 1) == 0
+    assert cu.cuStreamBeginCapture_v2(s, 2) == 0  # relaxed: no other call is concerned
+    assert cu.cuStreamSynchronize(s) != 0  # not allowed in a capture: it is broken now
+    with pytest.raises(fc.FlowCacheError, match="launch failed"):
+        fc.fc_rope(x, y, pos, plan, stream=s.value)
+    fc.fc_rope(x, y, pos, plan)
+    with pytest.raises(fc.FlowCacheError, match="error word"):
+        fc.fc_check_workspace(fc.FC_WS_IMPORTANCE, fc.workspace(256), stream=s.value)
+    g = vp()
+    assert cu.cuStreamEndCapture(s, ctypes.byref(g)) != 0
+    fc.fc_rope(x, y, pos, plan)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    assert cu.cuStreamDestroy_v2(s) == 0
