@@ -447,7 +447,9 @@ typedef struct {
  *                   k_i = clamp((orig_len w_i - beta_slow) /
  *                               (beta_fast - beta_slow), 0, 1),
  *                   and the factor m = 0.1 ln(factor) + 1 (m = 1 otherwise)
- * everything in float64.
+ * everything in float64.  YaRN's ramp is the published one, over the turns within the
+ * trained length; where a checkpoint was made with a ramp over the frequency's index
+ * between two rounded bounds, the frequencies in between differ: write them to `turns`.
  *   rot_dim   even, in [2, 256]
  *   base      > 1, finite
  *   factor    >= 1, finite (ignored by FC_ROPE_PLAIN)
@@ -456,6 +458,12 @@ typedef struct {
  *   n_axes    1 to 3 position axes (a video token has frame, row and column)
  *   sections  [n_axes] frequencies of each axis, in order, summing to
  *             rot_dim/2; NULL (n_axes must then be 1) for one axis
+ * The sections cut ONE ladder of frequencies.  Video models often give each axis a
+ * ladder of its own (theta starts again, with that axis's elements for rot_dim): fill a
+ * plan for each axis alone and copy its turns[0 .. section) into this plan's `turns`,
+ * one axis behind the other.  Whoever writes `turns` (any finite numbers) leaves the
+ * other fields as they are.  FC_ROPE_HALF pairs elements over the whole rotated part,
+ * FC_ROPE_INTERLEAVED neighbours, so that an axis's elements stay together.
  * Errors -> FC_ERR_INVALID_ARG, the plan untouched.  No device is used.
  */
 fc_status fc_rope_init(fc_rope_plan* plan, int rot_dim, fc_rope_layout layout, double base,
@@ -574,9 +582,11 @@ size_t fc_kv4_attention_workspace_size(fc_dtype dtype, int N, int Hq, int Hkv, i
  *            fc_kv_importance's (zero it once; read it with
  *            fc_check_workspace, FC_WS_IMPORTANCE)
  * The codes enter the tensor cores as float16, which holds code * scale
- * exactly.  Queries enter as float16 after a power of two per row (FC_F32: as a
- * sum of two), probabilities as float16 (FC_F32: a sum of two); sums are
- * float32.  What rows at and behind len_n hold is not used, NaN scales
+ * exactly.  Queries enter as float16 after a power of two per row: elements down
+ * to 2^-28 of the row's largest keep the bits of bf16 (FC_F32: a sum of two, 22
+ * bits).  Probabilities enter as float16, 11 bits (FC_F32: a sum of two, 22), in
+ * front of the values, while the sum that divides takes them in float32; sums are
+ * float32, and a result rounds once (bf16: behind a quotient of 2 ulps of float32).  What rows at and behind len_n hold is not used, NaN scales
  * included; a NaN that a query sees makes its whole row NaN, and one that it
  * does not see leaves it alone.
  * Errors: bad sizes, strides or pointers -> FC_ERR_INVALID_ARG; d not 64 or 128

@@ -6,6 +6,7 @@ import torch
 
 import cache_gating_kv_b200 as fc
 from oracle import kv4_oracle as O
+from tests.test_kv4_host import axis_ladders
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -156,3 +157,28 @@ def test_rope_on_a_stream_and_in_a_graph():
     fc.fc_rope(x, want, pos, plan)
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sections", [[22, 21, 21], [8, 12, 12], [5, 0, 3]])
+def test_rope_with_a_ladder_for_each_axis(sections, dtype):
+    """Frame, row and column parts of a video token's heads, each rotated as by itself."""
+    g = torch.Generator().manual_seed(9)
+    N, H, F, R, C = 2, 3, 3, 5, 4
+    L, d = F * R * C, 2 * sum(sections)
+    plan = axis_ladders(sections)
+    t = torch.arange(L)
+    pos = torch.stack([t // (R * C) + 7, t // C % R, t % C]).to(torch.int32)[:, None].repeat(1, N, 1)
+    x = torch.randn(N, H, L, d, generator=g).to(dtype)
+    y = torch.empty(N, H, L, d, dtype=dtype, device=DEV)
+    fc.fc_rope(x.to(DEV), y, pos.to(DEV), plan)
+    got, xn = y.double().cpu().numpy(), x.double().numpy()
+    at = 0
+    for a, n in enumerate(sections):
+        if n:
+            w, _ = O.rope_turns(2 * n)
+            part = xn[..., at:at + 2 * n]
+            want = O.rope(part, pos[a:a + 1].numpy(), w, interleaved=True)
+            # (the turns agree to 1e-14: at positions below 16 that is nothing to float32)
+            assert (np.abs(got[..., at:at + 2 * n] - want) <= _bound(part, want, 1.0, dtype)).all()
+        at += 2 * n

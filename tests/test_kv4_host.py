@@ -205,3 +205,21 @@ def test_arrays_that_are_read_must_be_apart_from_what_is_written():
     assert _refused(attend(lens=_fake(10) + 16))
     assert _refused(attend(lse=_fake(8))) and _refused(attend(lse=_fake(9))) and _refused(attend(lse=_fake(10)))
     assert _refused(attend(lse=_fake(3)))
+
+
+def axis_ladders(sections, layout=fc.FC_ROPE_INTERLEAVED):
+    """A plan whose axes have a ladder of frequencies each, made as documented."""
+    plan = fc.fc_rope_init(2 * sum(sections), layout, sections=sections)
+    at = 0
+    for n in sections:
+        plan.turns[at:at + n] = fc.fc_rope_init(2 * n).turns[:n] if n else []
+        at += n
+    return plan
+
+
+def test_plan_with_a_ladder_for_each_axis():
+    sections = [22, 21, 21]
+    p = axis_ladders(sections)
+    want = np.concatenate([10000.0 ** (-2.0 * np.arange(n) / (2 * n)) / (2 * np.pi) for n in sections])
+    np.testing.assert_allclose(np.array(p.turns[:64]), want, rtol=1e-14)
+    assert list(p.axis[:64]) == [0] * 22 + [1] * 21 + [2] * 21 and p.m == 1.0
