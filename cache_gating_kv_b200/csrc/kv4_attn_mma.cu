@@ -28,10 +28,15 @@
 //     computed beside the values of this one (81 -> 78 us).  The warps are joined at
 //     the end of a unit, and units that blocks share by a second, small kernel.
 // Per 32 keys a warp issues about 520 instructions, 128 of them conversions and 128
-// multiplications; at 16 warps an SM (120 registers; 24 warps of 80 spill and take
-// 92 us for 76) the schedulers issue in 3 of 5 cycles, which is what bounds it now:
-// 75 us for 312 MB (63 % of the measured copy rate), 37 us for one sequence of 131072
-// keys and 8 key heads (62 %); the same without any arithmetic takes 55 and 28.
+// multiplications, at 16 warps an SM (120 registers; 24 warps of 80 spill and take
+// 92 us for 76).  No unit is full: with four warps to a scheduler it issues in half of
+// the cycles, and of the 7.4 cycles from one instruction of a warp to its next 1.1 go to
+// other warps, 1.0 each to the latency of arithmetic, to full math pipes and to fetching
+// instructions, 0.7 to the block's barriers between units and 0.5 to dispatch (loads
+// are hardly among them).  72 to 78 us for 312 MB, over several boxes (61 to 66 % of
+// the measured copy rate), 36 to 38 us for one sequence of 131072 keys and 8 key heads
+// (62 %); the same without any arithmetic takes 55 and 28.  16 rows to a key head (two
+// n8 tiles, 128 registers with some spilled): 63 us for 151 MB, which 8 rows take 40 for.
 // The running maximum only moves when a step exceeds it by 2^8 (float16
 // probabilities, offset by 2^5, keep 11 bits over that range); for float32
 // queries it is exact, and queries and probabilities are sums of two float16
@@ -686,7 +691,9 @@ cudaError_t join(const AttnArgs& a, int N, cudaStream_t s) {
 // The tcgen05 kernel computes 128 rows whatever there are, this one reads the keys
 // once more for every 16.  Measured at 128 key heads x 8192 keys: d = 128, 32 rows
 // 106 us here and 134 there, 48 rows 152 and 136; d = 64, 24 rows 59 and 112, and
-// 24 heads x 1000 keys with 64 rows 15 and 21.
+// 24 heads x 1000 keys with 64 rows 15 and 21.  (The bytes alone take 23 and 11.5 us:
+// between 9 and 64 rows both kernels are four to six times from them, this one for
+// converting every key again, the other for computing rows that there are not.)
 bool use_tc(bool bf16, int R, int d) { return bf16 && R > (d == 128 ? 32 : 64); }
 
 struct Layout {
