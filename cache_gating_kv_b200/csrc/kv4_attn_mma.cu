@@ -33,7 +33,7 @@
 // the cycles, and of the 7.4 cycles from one instruction of a warp to its next 1.1 go to
 // other warps, 1.0 each to the latency of arithmetic, to full math pipes and to fetching
 // instructions, 0.7 to the block's barriers between units and 0.5 to dispatch (loads
-// are hardly among them).  72 to 78 us for 312 MB, over several boxes (61 to 66 % of
+// are hardly among them).  72 to 78 us for 312 MB, over several GPUs (61 to 66 % of
 // the measured copy rate), 36 to 38 us for one sequence of 131072 keys and 8 key heads
 // (62 %); the same without any arithmetic takes 55 and 28.  16 rows to a key head (two
 // n8 tiles, 128 registers with some spilled): 63 us for 151 MB, which 8 rows take 40 for.
