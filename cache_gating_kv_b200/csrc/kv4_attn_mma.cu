@@ -474,10 +474,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || NR == 1 ? 2 : 1)
           const uint32_t av[4] = {hmul2(e0[y], sab), hmul2(o0[y], sab), hmul2(e1[y], scd),
                                   hmul2(o1[y], scd)};
 #pragma unroll
-          for (int m = 0; m < NR; ++m)
+          for (int m = 0; m < NR; ++m) {
+            if constexpr (kF32) {
+              // The tensor cores cut what they add to (2^-23 of it, always downwards: 2e-6
+              // of a result over 40000 keys), so 16 keys are added by themselves and
+              // their sum to nearest.
+              float part[4];
+              mma_first(part, av, pb[m][P - 1][u][0], pb[m][P - 1][u][1]);
+              mma_add(part, av, pb[m][0][u][0], pb[m][0][u][1]);
 #pragma unroll
-            for (int q = 0; q < P; ++q)
-              mma_add(acc[m][4 * x + y], av, pb[m][q][u][0], pb[m][q][u][1]);
+              for (int c = 0; c < 4; ++c) acc[m][4 * x + y][c] += part[c];
+            } else {
+              mma_add(acc[m][4 * x + y], av, pb[m][0][u][0], pb[m][0][u][1]);
+            }
+          }
         }
       }
     }

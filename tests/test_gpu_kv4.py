@@ -493,6 +493,33 @@ def test_attention_f32_divides_exactly(keys, d):
         assert torch.equal(out, got[1][:, :, :1].repeat_interleave(2, 1).expand_as(out)), n
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 12])
+def test_attention_f32_sums_are_not_biased(G, d):
+    """Values of six (code 6, scale 1), float32: the result is six times the sum of the probabilities over itself,
+    by the two ways in which the kernel adds them, over 256 x G rows of 8192 keys each, so its mean over the rows
+    shows whether one of them leans to a side.
+
+    Roundings to nearest have no mean: 64 steps of a warp and the join of eight warps, in
+    numerator and denominator, each at most 2^-24, are 2^-24 sqrt(2 x 72 / 3) = 7 x 2^-24 a
+    row in the root mean square, 6 deviations of the mean over 256 rows 2.6 x 2^-24.  One
+    product on the tensor cores may cut what it adds: 16 products of a step and the two
+    terms of the probabilities, half of 2^-24 each at most of their largest and on average
+    half of that, below 2^-24 of their sum.  The quotient and its result round to nearest.
+    2^-22 in all.  (128 sums one behind the other, cut at 2^-23 of what they have reached,
+    would lean by some 128 / 4 x 2^-23 = 2^-18.)"""
+    g = torch.Generator().manual_seed(67)
+    N, H, keys = 64, 4, 8192
+    one = fc.fc_kv4_cache(1, 1, keys, d)
+    fc.fc_kv4_store(_randn(g, 1, 1, keys, d).to(DEV), torch.full((1, 1, keys, d), 6.0, device=DEV), one)
+    c = fc.Kv4Cache(*[t.expand(N, H, -1, -1).contiguous()
+                      for t in (one.k_codes, one.k_scales, one.v_codes, one.v_scales)])
+    q = _randn(g, N, H * G, 1, d).to(DEV)
+    out, _ = _attend(q, c, keys)
+    off = out.double()[..., 0].mean().item() / 6 - 1
+    assert abs(off) <= 2.0 ** -22, f"{off * 2 ** 24:.2f} x 2^-24"
+
+
 def test_attention_refusals():
     c = fc.fc_kv4_cache(2, 2, 32, 64)
     q = torch.zeros(2, 4, 3, 64, device=DEV, dtype=BF16)
